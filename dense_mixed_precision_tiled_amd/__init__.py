@@ -27,6 +27,8 @@ __all__ = [
     "gemm_num_configs", "gemm_config_name", "gemm_select_config",
     "GEMM_ACT_NONE", "GEMM_ACT_RELU", "GEMM_ACT_GELU", "GemmEpilogue",
     "gemm_run_ex", "gemm_run_ex_config", "gemm_validate_ex",
+    "gemm_quantize_rows", "gemm_validate_quantize_rows",
+    "gemm_run_scaled", "gemm_validate_scaled",
     "gemm_autotune", "gemm_autotune_lookup", "gemm_autotune_clear",
 ]
 
@@ -76,6 +78,12 @@ SIGNATURES = {
     "gemm_run_ex_config": (_int, [_int] + _GEMM_ARGS[:-1] + [ctypes.POINTER(GemmEpilogue), _vp]),
     "gemm_validate_ex": (_int, [_i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _int, _vp, _i64,
                                 _vp, _i64, _int, _int, _int, ctypes.POINTER(GemmEpilogue)]),
+    "gemm_quantize_rows": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp]),
+    "gemm_validate_quantize_rows": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp]),
+    "gemm_run_scaled": (_int, _GEMM_ARGS[:9] + [_vp, _vp] + _GEMM_ARGS[9:-1] +
+                        [ctypes.POINTER(GemmEpilogue), _vp]),
+    "gemm_validate_scaled": (_int, _GEMM_ARGS[:9] + [_vp, _vp] + _GEMM_ARGS[9:-2] +
+                             [ctypes.POINTER(GemmEpilogue)]),
     "gemm_autotune": (_int, _GEMM_ARGS[:-1] + [ctypes.POINTER(GemmEpilogue), _int,
                                               ctypes.POINTER(_int), _vp]),
     "gemm_autotune_lookup": (_int, [_i64, _i64, _i64, _int, _int, _int, _int, _int, _int]),
@@ -187,6 +195,38 @@ def gemm_validate_ex(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd,
     return library().gemm_validate_ex(M, N, K, A or None, lda, layoutA, B or None, ldb,
                                       layoutB, C or None, ldc, D or None, ldd, in_dtype,
                                       acc_dtype, out_dtype, _epi_ref(epi))
+
+
+def gemm_quantize_rows(M, K, X, ldx, in_dtype, Q, ldq, scales, stream) -> int:
+    """Enqueue the quantisation of X's rows to int8 ``Q`` with one fp32 scale
+    for each row; returns the status code."""
+    return library().gemm_quantize_rows(M, K, X or None, ldx, in_dtype, Q or None, ldq,
+                                        scales or None, stream or None)
+
+
+def gemm_validate_quantize_rows(M, K, X, ldx, in_dtype, Q, ldq, scales) -> int:
+    """Host-only argument check of gemm_quantize_rows; returns the status code."""
+    return library().gemm_validate_quantize_rows(M, K, X or None, ldx, in_dtype, Q or None, ldq,
+                                                 scales or None)
+
+
+def gemm_run_scaled(M, N, K, A, lda, layoutA, B, ldb, layoutB, scaleA, scaleB, C, ldc, D, ldd,
+                    in_dtype, acc_dtype, out_dtype, satf, epi, stream) -> int:
+    """Enqueue D = act(alpha * (A x B) * scaleA[i] * scaleB[j] + beta * C + bias)
+    of int8 A and B (``epi``: a GemmEpilogue or None); returns the status code."""
+    return library().gemm_run_scaled(M, N, K, A or None, lda, layoutA, B or None, ldb, layoutB,
+                                     scaleA or None, scaleB or None, C or None, ldc, D or None,
+                                     ldd, in_dtype, acc_dtype, out_dtype, int(satf),
+                                     _epi_ref(epi), stream or None)
+
+
+def gemm_validate_scaled(M, N, K, A, lda, layoutA, B, ldb, layoutB, scaleA, scaleB, C, ldc, D,
+                         ldd, in_dtype, acc_dtype, out_dtype, epi) -> int:
+    """Host-only argument check of gemm_run_scaled; returns the status code."""
+    return library().gemm_validate_scaled(M, N, K, A or None, lda, layoutA, B or None, ldb,
+                                          layoutB, scaleA or None, scaleB or None, C or None,
+                                          ldc, D or None, ldd, in_dtype, acc_dtype, out_dtype,
+                                          _epi_ref(epi))
 
 
 def gemm_autotune(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd,

@@ -11,6 +11,7 @@
 
 #include "../../include/libgemm.h"
 #include "gemm_configs.hpp"
+#include "gemm_host.hpp"
 #include "gemm_validate.hpp"
 
 using namespace libgemm;
@@ -55,6 +56,35 @@ __global__ void __launch_bounds__(256) repack_lines_kernel(const T *src, int64_t
 }
 
 }  // namespace libgemm
+
+namespace libgemm_host {
+namespace {
+constexpr Topology kDefaultTopology = {256, 8};
+std::mutex g_topo_mutex;
+Topology g_topo[kMaxDevices];
+bool g_topo_known[kMaxDevices];
+}  // namespace
+
+Topology topology() {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
+        return kDefaultTopology;
+    std::lock_guard<std::mutex> lock(g_topo_mutex);
+    if (!g_topo_known[dev]) {
+        Topology t = kDefaultTopology;
+        int v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
+            v > 0)
+            t.cus = v;
+        v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeNumberOfXccs, dev) == hipSuccess && v > 0)
+            t.xcds = v;
+        g_topo[dev] = t;
+        g_topo_known[dev] = true;
+    }
+    return g_topo[dev];
+}
+}  // namespace libgemm_host
 
 namespace {
 
@@ -129,40 +159,6 @@ int class_large(int klass) {
     return klass == 1 ? CFG_I8_LARGE8 : klass == 2 ? CFG_F8_LARGE : CFG_LARGE8;
 }
 
-
-// Compute units and XCDs of the current device, read once per device from
-// its attributes (MI355X: 256 CUs in 8 XCDs, which is also the answer when no
-// device can be queried, e.g. for gemm_select_config on a host without GPU).
-struct Topology {
-    int cus, xcds;
-};
-constexpr int kMaxDevices = 64;
-constexpr Topology kDefaultTopology = {256, 8};
-std::mutex g_topo_mutex;
-Topology g_topo[kMaxDevices];
-bool g_topo_known[kMaxDevices];
-
-Topology topology() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
-        return kDefaultTopology;
-    std::lock_guard<std::mutex> lock(g_topo_mutex);
-    if (!g_topo_known[dev]) {
-        Topology t = kDefaultTopology;
-        int v = 0;
-        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
-            v > 0)
-            t.cus = v;
-        v = 0;
-        if (hipDeviceGetAttribute(&v, hipDeviceAttributeNumberOfXccs, dev) == hipSuccess && v > 0)
-            t.xcds = v;
-        g_topo[dev] = t;
-        g_topo_known[dev] = true;
-    }
-    return g_topo[dev];
-}
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int select_config(int64_t M, int64_t N, int64_t K, int klass, int cus) {
     (void)K;

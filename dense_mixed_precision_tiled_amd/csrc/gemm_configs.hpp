@@ -102,6 +102,12 @@ hipError_t launch_skinny_i8(const Params &, int, int, int, dim3, hipStream_t);
 hipError_t launch_large_dma8_i8(const Params &, int, int, int, dim3, hipStream_t);
 hipError_t launch_large_dma16_i8(const Params &, int, int, int, dim3, hipStream_t);
 
+// the int8 tiles with scaled sums (gemm_run_scaled): kernels_<entry>_i8s.hip
+hipError_t launch_large8_i8s(const Params &, int, int, int, dim3, hipStream_t);
+hipError_t launch_medium_i8s(const Params &, int, int, int, dim3, hipStream_t);
+hipError_t launch_small_i8s(const Params &, int, int, int, dim3, hipStream_t);
+hipError_t launch_large_dma16_i8s(const Params &, int, int, int, dim3, hipStream_t);
+
 // fp8 entries, one translation unit per (entry, format): kernels_<entry>_f8.hip
 // (E4M3) and kernels_<entry>_bf8.hip (E5M2); the bf flag of launch_fn selects
 // E5M2

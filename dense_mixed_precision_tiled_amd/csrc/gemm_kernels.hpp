@@ -55,8 +55,10 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 // dtype codes of the C ABI (C, D and out_dtype)
 enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_I8 = 3, DT_I32 = 4 };
-// input (A, B) element types of the kernels: fp16, bf16, int8, OCP fp8 E4M3, E5M2
-enum { IT_F16 = 0, IT_BF16 = 1, IT_I8 = 2, IT_FP8 = 3, IT_BF8 = 4 };
+// input (A, B) element types of the kernels: fp16, bf16, int8, OCP fp8 E4M3, E5M2;
+// IT_I8S: int8 whose int32 sums are scaled by row and column into a float
+// output (scaled_epilogue)
+enum { IT_F16 = 0, IT_BF16 = 1, IT_I8 = 2, IT_FP8 = 3, IT_BF8 = 4, IT_I8S = 5 };
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 // Compile-time loop: f(integral_constant<int, I>) for I in [B, E).  Keeps
@@ -103,6 +105,8 @@ struct Params {
     int bias_rows;
     int act;            // ACT_*
     int c_col;          // C column-major: C(i,j) = C[j*ldc + i]
+    // IT_I8S: the sum is multiplied by row_scale[i] * col_scale[j] (nullptr: 1)
+    const float *row_scale, *col_scale;
 };
 
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2 };
@@ -1873,6 +1877,109 @@ __device__ __forceinline__ void tile_epilogue(const Params &p,
     }
 }
 
+// The epilogue of the scaled int8 products (IT_I8S, float outputs):
+//   D(i,j) = act(alpha * (n * row_scale[i] * col_scale[j]) + beta * C + bias)
+// with n the exact int32 sum, rounded to fp32 first (relative 2^-24).  The row
+// scale is applied before the column scale: their product alone could leave
+// the range of fp32.
+// Every tile is staged through LDS, one MF-row block per wave at a time, and
+// finished in a loop that is not unrolled: a lane then owns the same four
+// columns of every row it finishes, so the columns' scales and bias are eight
+// registers for the whole tile, and a wave stores whole row segments (256
+// bytes of 16-bit outputs at 128 columns) instead of 8 bytes in each of 16
+// rows.  (In registers, as tile_epilogue finishes interior tiles, the scales
+// of a lane's rows and columns and the three output types made the eight-wave
+// kernels spill 100 to 550 registers.)  Row values are staged in LDS as well: a
+// load from memory between two stores waits for both.
+template <class CF, int SMEM_BYTES, bool AGPR>
+__device__ __forceinline__ void scaled_epilogue(
+    const Params &p, typename AccT<CF::MF>::type (&acc)[CF::TM][CF::TN], int m0, int n0,
+    u32x4 *smem, int tid) {
+    constexpr int MF = CF::MF, TM = CF::TM, TN = CF::TN, WTN = CF::WTN;
+    constexpr int NG = AccT<MF>::N / 4;
+    constexpr int SROW = WTN + 8;  // words per staged row, padded against bank conflicts
+    constexpr int LPR = WTN / 4, RPP = 64 / LPR;
+    constexpr int WAVES = CF::WAVES_M * CF::WAVES_N;
+    static_assert(64 % LPR == 0 && MF % RPP == 0, "lanes per staged row");
+    static_assert((WAVES * MF * SROW + 2 * WAVES * CF::WTM) * 4 <= SMEM_BYTES,
+                  "staging fits in the operand buffers");
+    const int lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+    float *const stage = reinterpret_cast<float *>(smem) + wave * MF * SROW;
+    float *const rows = reinterpret_cast<float *>(smem) + WAVES * MF * SROW + wave * 2 * CF::WTM;
+    const int row0 = m0 + wm * CF::WTM;
+    const int c4 = (lane % LPR) * 4, gj = n0 + wn * WTN + c4;
+    for (int r = lane; r < CF::WTM; r += 64) {
+        const int gi = min(row0 + r, p.M - 1);
+        rows[r] = p.row_scale ? p.row_scale[gi] : 1.0f;
+        rows[CF::WTM + r] = (p.bias && p.bias_rows) ? p.bias[gi] : 0.0f;
+    }
+    f32x4 scol, bcol;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int gc = min(gj + e, p.N - 1);
+        scol[e] = p.col_scale ? p.col_scale[gc] : 1.0f;
+        bcol[e] = (p.bias && !p.bias_rows) ? p.bias[gc] : 0.0f;
+    }
+    const bool gin = p.cd_vec && gj + 4 <= p.N;
+    // C(gi, gj..gj+3); what lies outside M x N is not read and not stored
+    auto load_c4 = [&](int gi) {
+        f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (gi < p.M) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (gj + e < p.N) c[e] = load_c(p, gi, gj + e);
+        }
+        return c;
+    };
+#pragma nounroll
+    for (int i = 0; i < TM; ++i) {
+        Unroll<0, TM>::run([&](auto ii) {
+            constexpr int ic = decltype(ii)::value;
+            if (ic != i) return;
+            Unroll<0, TN>::run([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                Unroll<0, NG>::run([&](auto gg) {
+                    constexpr int g = decltype(gg)::value;
+                    *reinterpret_cast<f32x4 *>(stage + acc_row<MF>(lane) * SROW + j * MF +
+                                               acc_col<MF>(lane, g)) =
+                        acc_group<AGPR>(acc[ic][j], g);
+                });
+            });
+        });
+        // (LDS operations of one wave complete in order; this only keeps the
+        // compiler from moving the reads above the writes)
+        __builtin_amdgcn_wave_barrier();
+#pragma nounroll
+        for (int rr = lane / LPR; rr < MF; rr += RPP) {
+            const int gi = row0 + i * MF + rr;
+            const i32x4 n = *reinterpret_cast<const i32x4 *>(stage + rr * SROW + c4);
+            const float srow = rows[i * MF + rr], brow = rows[CF::WTM + i * MF + rr];
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = p.alpha * ((float)n[e] * srow * scol[e]) + bcol[e] + brow;
+            if (p.C) {
+                const f32x4 c = load_c4(gi);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += p.beta * c[e];
+            }
+            const bool full = gin && gi < p.M;
+            if (p.out_dtype == DT_F32) {
+                if (full) finish4<DT_F32, true, true, true>(p, gi, gj, v);
+                else finish4<DT_F32, false, true, true>(p, gi, gj, v);
+            } else if (p.out_dtype == DT_F16) {
+                if (full) finish4<DT_F16, true, true, true>(p, gi, gj, v);
+                else finish4<DT_F16, false, true, true>(p, gi, gj, v);
+            } else {
+                if (full) finish4<DT_BF16, true, true, true>(p, gi, gj, v);
+                else finish4<DT_BF16, false, true, true>(p, gi, gj, v);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // ------------------------------------------------------------------ kernel
 // VEC selects the vector (aligned) or the element-wise (unaligned) loads and
 // RAGGED whether the vector loads mask k >= kend; each combination is its own
@@ -1903,7 +2010,10 @@ __global__ void __launch_bounds__(CF::THREADS) gemm_mfma_kernel(Params p) {
     });
 
     k_loop<CF, IT, A_KC, B_KC, VEC, RAGGED>(p, m0, n0, kbeg, kend, acc, sA, sB, tid);
-    tile_epilogue<CF, IT, VEC, (int)sizeof(smem), false, !RAGGED>(p, acc, m0, n0, smem, tid);
+    if constexpr (IT == IT_I8S)
+        scaled_epilogue<CF, (int)sizeof(smem), false>(p, acc, m0, n0, smem, tid);
+    else
+        tile_epilogue<CF, IT, VEC, (int)sizeof(smem), false, !RAGGED>(p, acc, m0, n0, smem, tid);
 }
 
 // Large tiles on the LDS-DMA K loop (operands with 16-byte aligned rows, in
@@ -1931,7 +2041,10 @@ __global__ void __launch_bounds__(CF::THREADS) gemm_dma_kernel(Params p) {
     });
     dma_k_loop<CF, IT, A_KC, B_KC, RAGGED>(p, m0, n0, kbeg, kend, acc,
                                            reinterpret_cast<char *>(smem), tid);
-    tile_epilogue<CF, IT, true, 2 * (BM + BN) * BK * CF::ES, true>(p, acc, m0, n0, smem, tid);
+    if constexpr (IT == IT_I8S)
+        scaled_epilogue<CF, 2 * (BM + BN) * BK * CF::ES, true>(p, acc, m0, n0, smem, tid);
+    else
+        tile_epilogue<CF, IT, true, 2 * (BM + BN) * BK * CF::ES, true>(p, acc, m0, n0, smem, tid);
     wait_vmcnt<0>();  // the sink's loads land before the workgroup's LDS is released
 }
 

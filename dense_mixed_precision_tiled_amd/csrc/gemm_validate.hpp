@@ -115,4 +115,43 @@ inline int validate(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
     return GEMM_OK;
 }
 
+// gemm_run_scaled: the dtypes and K first, then the checks of a product of
+// 8-bit values with float outputs (those of an fp8 product of these sizes),
+// then the scales.
+inline int validate_scaled(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int layoutA,
+                           const void *B, int64_t ldb, int layoutB, const float *scaleA,
+                           const float *scaleB, const void *C, int64_t ldc, const void *D,
+                           int64_t ldd, int in_dtype, int acc_dtype, int out_dtype,
+                           const gemm_epilogue_t *epi) {
+    if (in_dtype != GEMM_I8 || acc_dtype != GEMM_I32) return GEMM_ERR_UNSUPPORTED;
+    const int st = validate(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd,
+                            GEMM_FP8_E4M3, GEMM_F32, out_dtype, epi, 0);
+    if (st != GEMM_OK) return st;
+    if (K >= ((int64_t)1 << 17)) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (!epi) epi = &kPlainEpilogue;
+    const bool row = epi->layoutD == GEMM_ROW_MAJOR;
+    const Range rd = extent(D, row ? M : N, row ? N : M, ldd, out_size(out_dtype));
+    if (scaleA && overlap(extent(scaleA, 1, M, M, 4), rd)) return GEMM_ERR_ALIASING;
+    if (scaleB && overlap(extent(scaleB, 1, N, N, 4), rd)) return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
+inline int validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype,
+                                  const void *Q, int64_t ldq, const float *scales) {
+    const int64_t kMaxDim = 0x7fffffff, kMaxLd = (int64_t)1 << 40;
+    if (M < 0 || K < 0 || M > kMaxDim || K > kMaxDim) return GEMM_ERR_INVALID_DIM;
+    if (in_dtype != GEMM_F16 && in_dtype != GEMM_BF16 && in_dtype != GEMM_F32)
+        return GEMM_ERR_UNSUPPORTED;
+    if (ldx < 1 || ldx < K || ldx > kMaxLd) return GEMM_ERR_INVALID_LD;
+    if (ldq < 1 || ldq < K || ldq > kMaxLd) return GEMM_ERR_INVALID_LD;
+    if (M == 0) return GEMM_OK;
+    if (!scales || (K > 0 && (!X || !Q))) return GEMM_ERR_NULL_PTR;
+    const Range rx = extent(X, K > 0 ? M : 0, K, ldx, in_dtype == GEMM_F32 ? 4 : 2);
+    const Range rq = extent(Q, K > 0 ? M : 0, K, ldq, 1);
+    const Range rs = extent(scales, 1, M, M, 4);
+    if (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs)) return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
 }  // namespace libgemm_host

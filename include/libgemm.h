@@ -336,6 +336,86 @@ int gemm_validate_ex(int64_t M, int64_t N, int64_t K,
                      int in_dtype, int acc_dtype, int out_dtype,
                      const gemm_epilogue_t *epi);
 
+/* ============================================== quantised linear layers
+ *
+ * An int8 product with a scale for each row of A (a token) and each column of
+ * D (an output channel), and the operator that makes such an A from 16-bit or
+ * 32-bit activations.  Both enqueue exactly one kernel, allocate nothing and
+ * use no workspace, so they can be captured into a HIP graph, and calls on
+ * different streams do not touch each other.
+ *
+ * gemm_quantize_rows: for each row i of X (M x K, row-major, ldx >= K),
+ *
+ *   a = max_k |X(i,k)|,   scales[i] = a / 127,
+ *   Q(i,k) = X(i,k) * 127 / a, rounded to nearest even,
+ *
+ * so Q lies in [-127, 127] and X(i,k) = scales[i] * Q(i,k) to within half a
+ * step (scales[i] / 2).
+ *   in_dtype     GEMM_F16, GEMM_BF16 or GEMM_F32 (X).
+ *   Q, ldq       device pointer to int8 elements, row-major, ldq >= K.  Nothing
+ *                outside rows [0,M) and columns [0,K) is written.
+ *   scales       device pointer to M fp32 values.
+ * A row of zeros (or K == 0) gets scale 0 and zeros.  A row that holds an Inf or
+ * a NaN gets scale NaN and zeros, so that a product with it is NaN, not a
+ * number that looks right.
+ * Accuracy: Q is the correctly rounded value of the exact quotient (ties to
+ * even) for every finite row; scales[i] is a / 127 rounded once to fp32.
+ * Speed: 16-byte loads and stores where X and Q are 16-byte aligned with ldx
+ * and ldq multiples of 16 bytes; element by element otherwise.
+ * Errors: GEMM_ERR_INVALID_DIM, GEMM_ERR_INVALID_LD, GEMM_ERR_NULL_PTR (a
+ * pointer that a non-empty operation needs), GEMM_ERR_UNSUPPORTED (in_dtype),
+ * GEMM_ERR_ALIASING (X, Q and scales must not overlap), GEMM_ERR_HIP.
+ */
+int gemm_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype, void *Q,
+                       int64_t ldq, float *scales, void *stream);
+
+/* Host-only argument check of gemm_quantize_rows (see gemm_validate). */
+int gemm_validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype,
+                                const void *Q, int64_t ldq, const float *scales);
+
+/*
+ * gemm_run_scaled: D = act( alpha * (A x B)(i,j) * scaleA[i] * scaleB[j]
+ *                           + beta * C(i,j) + bias[j] ),
+ * A x B the exact int32 sum of int8 products, rounded once to out_dtype, then
+ * satf.  Arguments as for gemm_run_ex, with
+ *   in_dtype     GEMM_I8, acc_dtype GEMM_I32, out_dtype GEMM_F32, GEMM_F16 or
+ *                GEMM_BF16 (C and D), K < 2^17 (the int32 sum cannot wrap).
+ *   scaleA       device pointer to M fp32 values, one for each row of A, or
+ *                NULL (1).
+ *   scaleB       device pointer to N fp32 values, one for each column of B, or
+ *                NULL (1).
+ *   epi          gemm_epilogue_t (alpha, beta, bias, activation, layouts of C
+ *                and D), or NULL.
+ * Between the exact sum and the final rounding everything is fp32: the sum is
+ * rounded to fp32, multiplied by the row's scale, the column's scale and alpha
+ * in this order (three roundings, each 2^-24 relative), then beta * C and bias
+ * are added.  Where K == 0 the product is 0, whatever the scales.
+ * Errors as gemm_run_ex, and: another dtype combination, or K >= 2^17 ->
+ * GEMM_ERR_UNSUPPORTED; D overlapping scaleA or scaleB -> GEMM_ERR_ALIASING.
+ *
+ * Speed: vector loads as for gemm_run.  The int8 tiles, chosen by shape.
+ * Operands that miss the vector loads are read element by element (gemm_run
+ * copies large ones into its workspace first; this call has none).
+ */
+int gemm_run_scaled(int64_t M, int64_t N, int64_t K,
+                    const void *A, int64_t lda, int layoutA,
+                    const void *B, int64_t ldb, int layoutB,
+                    const float *scaleA, const float *scaleB,
+                    const void *C, int64_t ldc,
+                    void *D, int64_t ldd,
+                    int in_dtype, int acc_dtype, int out_dtype,
+                    int satf, const gemm_epilogue_t *epi, void *stream);
+
+/* Host-only argument check of gemm_run_scaled (see gemm_validate). */
+int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
+                         const void *A, int64_t lda, int layoutA,
+                         const void *B, int64_t ldb, int layoutB,
+                         const float *scaleA, const float *scaleB,
+                         const void *C, int64_t ldc,
+                         const void *D, int64_t ldd,
+                         int in_dtype, int acc_dtype, int out_dtype,
+                         const gemm_epilogue_t *epi);
+
 /* ============================================================ autotuning
  *
  * Runtime search over the tile-shape table for one problem signature,
