@@ -29,6 +29,7 @@ __all__ = [
     "gemm_run_ex", "gemm_run_ex_config", "gemm_validate_ex",
     "gemm_quantize_rows", "gemm_validate_quantize_rows",
     "gemm_run_scaled", "gemm_validate_scaled",
+    "GEMM_ACT_SILU", "GemmMoe", "gemm_moe_run", "gemm_moe_workspace", "gemm_validate_moe",
     "gemm_autotune", "gemm_autotune_lookup", "gemm_autotune_clear",
 ]
 
@@ -36,7 +37,7 @@ GEMM_ROW_MAJOR, GEMM_COL_MAJOR = 0, 1
 GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_I8, GEMM_I32 = 0, 1, 2, 3, 4
 GEMM_FP8_E4M3, GEMM_FP8_E5M2 = 5, 6
 GEMM_OK = 0
-GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU = 0, 1, 2
+GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_SILU = 0, 1, 2, 3
 STATUS_NAMES = {
     0: "GEMM_OK", -1: "GEMM_ERR_INVALID_DIM", -2: "GEMM_ERR_INVALID_LD",
     -3: "GEMM_ERR_NULL_PTR", -4: "GEMM_ERR_UNSUPPORTED", -5: "GEMM_ERR_INVALID_LAYOUT",
@@ -58,6 +59,22 @@ class GemmEpilogue(ctypes.Structure):
     def __init__(self, alpha=1.0, beta=1.0, bias=0, activation=GEMM_ACT_NONE,
                  layoutC=GEMM_ROW_MAJOR, layoutD=GEMM_ROW_MAJOR):
         super().__init__(alpha, beta, bias or None, activation, layoutC, layoutD)
+
+
+class GemmMoe(ctypes.Structure):
+    """gemm_moe_t: a mixture-of-experts layer.
+
+    ``W1``, ``W2`` and the scales of int8 weights are device addresses (int)."""
+    _fields_ = [("H", ctypes.c_int64), ("I", ctypes.c_int64), ("E", ctypes.c_int64),
+                ("topk", ctypes.c_int64), ("W1", ctypes.c_void_p), ("ld1", ctypes.c_int64),
+                ("W2", ctypes.c_void_p), ("ld2", ctypes.c_int64), ("scale1", ctypes.c_void_p),
+                ("scale2", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("renormalize", ctypes.c_int)]
+
+    def __init__(self, H, I, E, topk, w_dtype, W1, ld1, W2, ld2, scale1=0, scale2=0,
+                 activation=GEMM_ACT_SILU, renormalize=False):
+        super().__init__(H, I, E, topk, W1 or None, ld1, W2 or None, ld2, scale1 or None,
+                         scale2 or None, w_dtype, activation, int(renormalize))
 
 
 # Exported symbols and their C signatures (mirrors include/libgemm.h).
@@ -84,6 +101,11 @@ SIGNATURES = {
                         [ctypes.POINTER(GemmEpilogue), _vp]),
     "gemm_validate_scaled": (_int, _GEMM_ARGS[:9] + [_vp, _vp] + _GEMM_ARGS[9:-2] +
                              [ctypes.POINTER(GemmEpilogue)]),
+    "gemm_moe_run": (_int, [_i64, ctypes.POINTER(GemmMoe), _vp, _i64, _vp, _i64, _vp, _i64, _int,
+                            _vp, _i64, _vp]),
+    "gemm_moe_workspace": (_i64, [_i64, ctypes.POINTER(GemmMoe)]),
+    "gemm_validate_moe": (_int, [_i64, ctypes.POINTER(GemmMoe), _vp, _i64, _vp, _i64, _vp, _i64,
+                                 _int, _vp, _i64]),
     "gemm_autotune": (_int, _GEMM_ARGS[:-1] + [ctypes.POINTER(GemmEpilogue), _int,
                                               ctypes.POINTER(_int), _vp]),
     "gemm_autotune_lookup": (_int, [_i64, _i64, _i64, _int, _int, _int, _int, _int, _int]),
@@ -227,6 +249,28 @@ def gemm_validate_scaled(M, N, K, A, lda, layoutA, B, ldb, layoutB, scaleA, scal
                                           layoutB, scaleA or None, scaleB or None, C or None,
                                           ldc, D or None, ldd, in_dtype, acc_dtype, out_dtype,
                                           _epi_ref(epi))
+
+
+def gemm_moe_run(T, layer, X, ldx, logits, ldl, D, ldd, in_dtype, workspace, workspace_bytes,
+                 stream) -> int:
+    """Enqueue the mixture-of-experts layer ``layer`` (a GemmMoe) on T tokens;
+    returns the status code."""
+    return library().gemm_moe_run(T, _epi_ref(layer), X or None, ldx, logits or None, ldl,
+                                  D or None, ldd, in_dtype, workspace or None, workspace_bytes,
+                                  stream or None)
+
+
+def gemm_moe_workspace(T, layer) -> int:
+    """Bytes of device workspace that gemm_moe_run needs, or a negative status code."""
+    return library().gemm_moe_workspace(T, _epi_ref(layer))
+
+
+def gemm_validate_moe(T, layer, X, ldx, logits, ldl, D, ldd, in_dtype, workspace,
+                      workspace_bytes) -> int:
+    """Host-only argument check of gemm_moe_run; returns the status code."""
+    return library().gemm_validate_moe(T, _epi_ref(layer), X or None, ldx, logits or None, ldl,
+                                       D or None, ldd, in_dtype, workspace or None,
+                                       workspace_bytes)
 
 
 def gemm_autotune(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd,

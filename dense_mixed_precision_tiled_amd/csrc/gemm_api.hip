@@ -718,7 +718,8 @@ const char *gemm_status_string(int status) {
     case GEMM_ERR_HIP: return "HIP runtime error";
     case GEMM_ERR_INVALID_CONFIG: return "no such tile-table entry";
     case GEMM_ERR_SCRATCH_TOO_SMALL:
-        return "split-K partial sums exceed the 32 MiB scratch of gemm_run_noalloc";
+        return "workspace too small (gemm_moe_run), or split-K partial sums exceed the 32 MiB "
+               "scratch of gemm_run_noalloc";
     default: return "unknown status";
     }
 }

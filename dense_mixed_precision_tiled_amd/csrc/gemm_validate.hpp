@@ -154,4 +154,73 @@ inline int validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t l
     return GEMM_OK;
 }
 
+// The layer's dimensions, and the workspace they need.
+inline int validate_moe_dims(int64_t T, const gemm_moe_t *m) {
+    if (!m) return GEMM_ERR_NULL_PTR;
+    const int64_t kMaxWidth = (int64_t)1 << 24;
+    if (T < 0 || m->H < 1 || m->I < 1 || m->H > kMaxWidth || m->I > kMaxWidth || m->E < 1 ||
+        m->topk < 1 || m->topk > m->E)
+        return GEMM_ERR_INVALID_DIM;
+    if (T > 64 || m->E > 1024 || m->topk > 32) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+// Offsets of the parts of the workspace, from its start rounded up to 256 bytes.
+struct MoeWorkspace {
+    int64_t slots, ldh;
+    int64_t count, expert, pairs, weight, h, bytes;
+};
+
+inline MoeWorkspace moe_workspace(int64_t T, const gemm_moe_t *m) {
+    MoeWorkspace w;
+    const int64_t npairs = T * m->topk;
+    w.slots = m->E < npairs ? m->E : npairs;
+    w.ldh = (m->I + 7) / 8 * 8;  // rows of whole 16 bytes
+    w.count = 0;
+    w.expert = w.count + 4 * w.slots;
+    w.pairs = w.expert + 4 * w.slots;
+    w.weight = w.pairs + 4 * w.slots * T;
+    w.h = (w.weight + 4 * npairs + 255) / 256 * 256;
+    w.bytes = w.h + 2 * npairs * w.ldh + 255;
+    return w;
+}
+
+inline int validate_moe(int64_t T, const gemm_moe_t *m, const void *X, int64_t ldx,
+                        const float *logits, int64_t ldl, const void *D, int64_t ldd, int in_dtype,
+                        const void *workspace, int64_t workspace_bytes) {
+    const int st = validate_moe_dims(T, m);
+    if (st != GEMM_OK) return st;
+    if (in_dtype != GEMM_F16 && in_dtype != GEMM_BF16) return GEMM_ERR_UNSUPPORTED;
+    if (m->w_dtype != in_dtype && m->w_dtype != GEMM_I8) return GEMM_ERR_UNSUPPORTED;
+    if (m->activation != GEMM_ACT_SILU && m->activation != GEMM_ACT_GELU &&
+        m->activation != GEMM_ACT_RELU)
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t kMaxLd = (int64_t)1 << 30;
+    auto ld_bad = [&](int64_t ld, int64_t inner) { return ld < inner || ld > kMaxLd; };
+    if (ld_bad(ldx, m->H) || ld_bad(ldl, m->E) || ld_bad(ldd, m->H) || ld_bad(m->ld1, m->H) ||
+        ld_bad(m->ld2, m->I))
+        return GEMM_ERR_INVALID_LD;
+    if (T == 0) return GEMM_OK;
+    const bool i8 = m->w_dtype == GEMM_I8;
+    if (!X || !logits || !D || !workspace || !m->W1 || !m->W2 ||
+        (i8 && (!m->scale1 || !m->scale2)))
+        return GEMM_ERR_NULL_PTR;
+    const int64_t need = moe_workspace(T, m).bytes;
+    if (workspace_bytes < need) return GEMM_ERR_SCRATCH_TOO_SMALL;
+    const int wsz = i8 ? 1 : 2;
+    const int64_t r1 = m->E * 2 * m->I, r2 = m->E * m->H;
+    const Range rd = extent(D, T, m->H, ldd, 2);
+    const Range rw = extent(workspace, 1, need, need, 1);
+    const Range in[6] = {extent(X, T, m->H, ldx, 2),
+                         extent(logits, T, m->E, ldl, 4),
+                         extent(m->W1, r1, m->H, m->ld1, wsz),
+                         extent(m->W2, r2, m->I, m->ld2, wsz),
+                         extent(m->scale1, i8 ? 1 : 0, r1, r1, 4),
+                         extent(m->scale2, i8 ? 1 : 0, r2, r2, 4)};
+    if (overlap(rd, rw)) return GEMM_ERR_ALIASING;
+    for (const Range &r : in)
+        if (overlap(r, rd) || overlap(r, rw)) return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
 }  // namespace libgemm_host

@@ -1,0 +1,10 @@
+// The mixture-of-experts kernels for bf16 activations and weights of the same type, in a
+// translation unit of its own so the library builds in parallel.
+#include "moe.hpp"
+
+namespace libgemm {
+hipError_t launch_moe_bf16(const MoeParams &p, int up_blocks, bool vec, hipStream_t s) {
+    return vec ? moe_launch<IT_BF16, false, true>(p, up_blocks, s)
+               : moe_launch<IT_BF16, false, false>(p, up_blocks, s);
+}
+}  // namespace libgemm

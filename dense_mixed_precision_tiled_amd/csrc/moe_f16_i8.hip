@@ -1,0 +1,10 @@
+// The mixture-of-experts kernels for f16 activations and int8 weights, in a
+// translation unit of its own so the library builds in parallel.
+#include "moe.hpp"
+
+namespace libgemm {
+hipError_t launch_moe_f16_i8(const MoeParams &p, int up_blocks, bool vec, hipStream_t s) {
+    return vec ? moe_launch<IT_F16, true, true>(p, up_blocks, s)
+               : moe_launch<IT_F16, true, false>(p, up_blocks, s);
+}
+}  // namespace libgemm

@@ -83,7 +83,8 @@ typedef enum {
     GEMM_ERR_INVALID_CONFIG = -8, /* gemm_run_config: no such config, or the
                                      config cannot run this problem            */
     GEMM_ERR_SCRATCH_TOO_SMALL = -9 /* gemm_run_noalloc: the split-K partial
-                                     sums need more than its fixed scratch     */
+                                     sums need more than its fixed scratch;
+                                     gemm_moe_run: workspace_bytes too small   */
 } gemm_status_t;
 
 /*
@@ -274,7 +275,8 @@ int gemm_validate(int64_t M, int64_t N, int64_t K,
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1,
-    GEMM_ACT_GELU = 2
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_SILU = 3  /* x / (1 + exp(-x)); gemm_moe_run only */
 } gemm_activation_t;
 
 typedef struct {
@@ -393,7 +395,9 @@ int gemm_validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx
  * Errors as gemm_run_ex, and: another dtype combination, or K >= 2^17 ->
  * GEMM_ERR_UNSUPPORTED; D overlapping scaleA or scaleB -> GEMM_ERR_ALIASING.
  *
- * Speed: vector loads as for gemm_run.  The int8 tiles, chosen by shape.
+ * Speed: vector loads as for gemm_run.  Calls with M <= 64 rows, K-contiguous
+ * operands (row-major A, column-major B) and vector loads stream B from memory
+ * once, a column block for each workgroup; other calls run the int8 tiles.
  * Operands that miss the vector loads are read element by element (gemm_run
  * copies large ones into its workspace first; this call has none).
  */
@@ -415,6 +419,88 @@ int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
                          const void *D, int64_t ldd,
                          int in_dtype, int acc_dtype, int out_dtype,
                          const gemm_epilogue_t *epi);
+
+/* ================================================ mixture of experts
+ *
+ * A whole mixture-of-experts layer for a few tokens (T <= 64: decoding), from
+ * the router's logits to the layer's output, in two kernels.  For each token t
+ * with logits l (the router's product, e.g. by gemm_run into fp32):
+ *
+ *   chosen   the topk experts of largest l, ties to the lower index
+ *   w_e    = exp(l_e) / sum over all experts of exp(l), or with renormalize
+ *            / sum over the chosen experts
+ *   h_e    = act(x G_e^T) * (x U_e^T)         elementwise, I values
+ *   y      = sum over the chosen e of w_e (h_e D_e^T)
+ *
+ * An expert at -Inf is not chosen, so a token may have fewer than topk experts;
+ * one whose logits are all -Inf has y = 0.  A token with a NaN or +Inf among
+ * its logits has y = NaN.  Experts that no token chose are not read.
+ *
+ * gemm_moe_t describes the layer:
+ *   H, I, E, topk   model width, inner width, experts (<= 1024), experts of a
+ *                token (<= 32, <= E); H, I in [1, 2^24]
+ *   w_dtype      GEMM_F16 or GEMM_BF16 (then the type of x), or GEMM_I8
+ *   W1, ld1      E x 2I rows of H elements, lines ld1 >= H elements apart: rows
+ *                [0, I) of an expert are its gate G, rows [I, 2I) its up U
+ *   W2, ld2      E x H rows of I elements, lines ld2 >= I elements apart: D
+ *   scale1, scale2   GEMM_I8: one fp32 scale for each row of W1 (E x 2I) and W2
+ *                (E x H), contiguous; the weight is scale * int8.  Else unused.
+ *   activation   act: GEMM_ACT_SILU, GEMM_ACT_GELU or GEMM_ACT_RELU
+ *   renormalize  nonzero: the chosen weights sum to 1
+ *
+ * gemm_moe_run:
+ *   T            tokens, 0 to 64.  T == 0: nothing to do, returns GEMM_OK.
+ *   X, ldx       T x H elements of in_dtype (GEMM_F16 or GEMM_BF16), row-major
+ *   logits, ldl  T x E fp32, row-major
+ *   D, ldd       T x H elements of in_dtype, row-major; nothing outside is written
+ *   workspace    device memory of at least gemm_moe_workspace(T, layer) bytes,
+ *                of any content, owned by the caller, written by the call.  A call
+ *                must not overlap another one (or a graph's replay) that uses the
+ *                same workspace, unless the caller orders them; calls with
+ *                workspaces of their own may overlap freely.
+ * The call enqueues two kernels and allocates nothing, so it can be captured
+ * into a HIP graph; the routing is found on the device, and a replay follows the
+ * logits of its own time.  The same call gives the same bits.
+ *
+ * Accuracy: products and sums are fp32, as are the softmax and everything
+ * between; h is rounded to in_dtype (the second product's operand; an fp16 h
+ * overflows to Inf past 65504) and y once at the end.  int8 weights are
+ * converted exactly and their scales applied to the fp32 sums.
+ *
+ * Speed: bound by the chosen experts' weights, each read once.  16-byte loads
+ * where X, W1 and W2 are 16-byte aligned with lines of whole 16 bytes; element
+ * by element otherwise (slow).
+ *
+ * Errors: GEMM_ERR_INVALID_DIM (T < 0; H, I, E or topk out of range above or
+ * topk > E), GEMM_ERR_UNSUPPORTED (T > 64, E > 1024, topk > 32, a dtype or
+ * activation not named above), GEMM_ERR_INVALID_LD, GEMM_ERR_NULL_PTR,
+ * GEMM_ERR_ALIASING (D or the workspace overlapping another argument),
+ * GEMM_ERR_SCRATCH_TOO_SMALL, GEMM_ERR_HIP (D is then not written).
+ */
+typedef struct {
+    int64_t H, I, E, topk;
+    const void *W1;
+    int64_t ld1;
+    const void *W2;
+    int64_t ld2;
+    const float *scale1, *scale2;
+    int w_dtype;
+    int activation;
+    int renormalize;
+} gemm_moe_t;
+
+int gemm_moe_run(int64_t T, const gemm_moe_t *layer, const void *X, int64_t ldx,
+                 const float *logits, int64_t ldl, void *D, int64_t ldd, int in_dtype,
+                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for T tokens, or a negative gemm_status_t (T, H, I, E or
+ * topk invalid or unsupported). */
+int64_t gemm_moe_workspace(int64_t T, const gemm_moe_t *layer);
+
+/* Host-only argument check of gemm_moe_run (see gemm_validate). */
+int gemm_validate_moe(int64_t T, const gemm_moe_t *layer, const void *X, int64_t ldx,
+                      const float *logits, int64_t ldl, const void *D, int64_t ldd, int in_dtype,
+                      const void *workspace, int64_t workspace_bytes);
 
 /* ============================================================ autotuning
  *
