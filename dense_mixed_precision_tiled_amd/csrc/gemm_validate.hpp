@@ -157,7 +157,7 @@ inline int validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t l
 // The layer's dimensions, and the workspace they need.
 inline int validate_moe_dims(int64_t T, const gemm_moe_t *m) {
     if (!m) return GEMM_ERR_NULL_PTR;
-    const int64_t kMaxWidth = (int64_t)1 << 24;
+    const int64_t kMaxWidth = (int64_t)1 << 19;
     if (T < 0 || m->H < 1 || m->I < 1 || m->H > kMaxWidth || m->I > kMaxWidth || m->E < 1 ||
         m->topk < 1 || m->topk > m->E)
         return GEMM_ERR_INVALID_DIM;
@@ -195,7 +195,8 @@ inline int validate_moe(int64_t T, const gemm_moe_t *m, const void *X, int64_t l
     if (m->activation != GEMM_ACT_SILU && m->activation != GEMM_ACT_GELU &&
         m->activation != GEMM_ACT_RELU)
         return GEMM_ERR_UNSUPPORTED;
-    const int64_t kMaxLd = (int64_t)1 << 30;
+    // (the kernels' row offsets are 32 bits: 64 rows of X, 2048 of h)
+    const int64_t kMaxLd = (int64_t)1 << 24;
     auto ld_bad = [&](int64_t ld, int64_t inner) { return ld < inner || ld > kMaxLd; };
     if (ld_bad(ldx, m->H) || ld_bad(ldl, m->E) || ld_bad(ldd, m->H) || ld_bad(m->ld1, m->H) ||
         ld_bad(m->ld2, m->I))

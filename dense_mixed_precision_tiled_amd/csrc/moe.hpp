@@ -16,6 +16,10 @@
 // and tokens by counting the logits above one (the rank of an expert is how
 // many are larger, or equal with a lower index), which needs no sorting and no
 // pass of its own: E / 64 loads and ballots for each token.
+//
+// One token's layer is mostly latency: the chain from the launch to the first
+// weights (logits, expert, tokens) is kept to one load from memory in each kernel,
+// with what follows from registers and LDS.
 #pragma once
 
 #include "stream.hpp"
@@ -28,7 +32,7 @@ struct MoeParams {
     const uint8_t *X, *W1, *W2;
     const float *logits, *s1, *s2;  // s1, s2: scales of int8 weights by row, or nullptr
     uint8_t *D;
-    int64_t ldx, ldl, ld1, ld2, ldd;  // elements
+    int64_t ldx, ldl, ld1, ld2, ldd;  // elements, at most 2^24: row offsets are 32 bits
     int T, H, I, E, topk, slots;
     int act, renorm;
     // workspace
@@ -55,15 +59,56 @@ __device__ __forceinline__ uint32_t moe_key(float l) {
 }
 constexpr uint32_t kMoeNone = 0x007fffffu;  // key of -Inf: such an expert is not chosen
 
-// Rank of expert e among the logits of one token: the whole wave counts.
-__device__ __forceinline__ int moe_rank(const float *l, int E, int e, uint32_t mine, int lane) {
+// Rank of expert e among the keys of one token (key(j) of expert j): the whole
+// wave counts.
+template <class Key>
+__device__ __forceinline__ int moe_rank(Key &&key, int E, int e, int lane) {
+    const uint32_t mine = key(e);
     int rank = 0;
     for (int j0 = 0; j0 < E; j0 += 64) {
         const int j = j0 + lane;
-        const uint32_t k = j < E ? moe_key(l[j]) : 0u;
+        const uint32_t k = j < E ? key(j) : 0u;
         rank += __popcll(__ballot(j < E && (k > mine || (k == mine && j < e))));
     }
-    return rank;
+    return mine > kMoeNone ? rank : kMoeMaxExperts;
+}
+
+// Largest value of the wave, in every lane.
+__device__ __forceinline__ uint32_t moe_wave_max(uint32_t v) {
+    auto step = [&](auto ctrl, auto rows) {
+        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
+                                                         decltype(rows)::value, 0xf, false));
+    };
+    using All = std::integral_constant<int, 0xf>;
+    step(std::integral_constant<int, 0x111>{}, All{});  // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>{}, All{});
+    step(std::integral_constant<int, 0x114>{}, All{});
+    step(std::integral_constant<int, 0x118>{}, All{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast 15
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast 31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The expert of rank r among at most 256, or -1 (r experts or fewer above -Inf):
+// the largest is taken out r times.  The whole wave, no LDS.
+__device__ __forceinline__ int moe_expert_of_rank(const float *l, int E, int r, int lane) {
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = lane + 64 * i < E ? moe_key(l[lane + 64 * i]) : 0u;
+    for (;; --r) {
+        const uint32_t m = moe_wave_max(max(max(k[0], k[1]), max(k[2], k[3])));
+        if (m <= kMoeNone) return -1;
+        int e = -1;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const uint64_t b = __ballot(k[i] == m);
+            if (b) e = 64 * i + (int)__builtin_ctzll(b);
+        }
+        if (r == 0) return e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e == lane + 64 * i) k[i] = 0u;
+    }
 }
 
 template <int IT>
@@ -91,7 +136,7 @@ __device__ __forceinline__ void moe_store4(uint8_t *row, int64_t j, int n, bool 
 // or over the chosen ones.  A row with a NaN or +Inf gives NaN, a row of -Inf
 // zeros; an expert at -Inf has weight 0.  The 256 threads of the workgroup.
 __device__ inline void moe_weights(const MoeParams &p, int t, uint32_t *keys, float *part) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const float *l = p.logits + (int64_t)t * p.ldl;
     __syncthreads();  // keys and part of the token before
     float top = -__builtin_inff();
@@ -139,52 +184,77 @@ __device__ inline void moe_weights(const MoeParams &p, int t, uint32_t *keys, fl
 // Slot blockIdx.y, columns of h in blocks of 16, one for each workgroup in
 // turn; the last workgroup of a slot (blockIdx.x == gridDim.x - 1) writes the
 // slot's tokens and the weights of token blockIdx.y, blockIdx.y + slots, ...
-// instead.  MT: row groups of 16 tokens; four waves split H.
+// instead.  Four waves split H.  MT: row groups of 16 tokens in one pass over the
+// weights (1 for T <= 16, 2 otherwise), or 0 for T <= 4; an expert of few tokens
+// takes a shorter pass, one of more than 32 several.
+constexpr int kMoeStaged = 4096;  // logits (or pairs) that are held in LDS
+
 template <int IT, bool W8, int MT, bool VEC>
 __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
-    constexpr int U = MT == 4 ? 1 : (MT == 2 ? 2 : (W8 ? 2 : 4));
-    __shared__ uint32_t keys[kMoeMaxExperts];
+    __shared__ uint32_t keys[kMoeStaged];
     __shared__ float part[8];
     __shared__ int ranks[kMoeMaxTokens], list[kMoeMaxTokens], found[2];
-    __shared__ f32x4 sums[4][2 * MT][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int slot = blockIdx.y;
+    constexpr int ROWS = MT == 0 ? 4 : 16 * MT;  // tokens of a pass
+    __shared__ f32x4 sums[4][MT == 2 ? 4 : 2][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int slot = blockIdx.y, t0 = slot / p.topk, r0 = slot % p.topk;
+    const bool own = p.slots != p.E;  // the slot is token t0's expert of rank r0
+    const bool staged = p.T * p.E <= kMoeStaged;
 
-    // the slot's expert
-    int e = slot, t0 = 0;
-    if (p.slots != p.E) {
-        t0 = slot / p.topk;
-        const int r0 = slot % p.topk;
-        const float *l = p.logits + (int64_t)t0 * p.ldl;
-        for (int j = tid; j < p.E; j += 256) keys[j] = moe_key(l[j]);
+    int e = slot, n;
+    if (own && p.T == 1 && p.E <= 256) {
+        e = moe_expert_of_rank(p.logits, p.E, r0, lane);
+        n = e >= 0 ? 1 : 0;
+        if (tid == 0) list[0] = r0;
         __syncthreads();
-        for (int j = tid; j < p.E; j += 256) {
-            const uint32_t mine = keys[j];
-            int rank = 0;
-            for (int i = 0; i < p.E; ++i) rank += keys[i] > mine || (keys[i] == mine && i < j);
-            if (rank == r0) found[0] = j;  // ranks are 0 .. E - 1, each once
+    } else {
+        auto key = [&](int t, int j) {
+            return staged ? keys[t * p.E + j] : moe_key(p.logits[(int64_t)t * p.ldl + j]);
+        };
+        if (staged) {
+            for (int i = tid; i < p.T * p.E; i += 256)
+                keys[i] = moe_key(p.logits[(int64_t)(i / p.E) * p.ldl + i % p.E]);
+            __syncthreads();
+        }
+        if (own) {
+            if (p.E <= 256) {
+                e = moe_expert_of_rank(p.logits + (int64_t)t0 * p.ldl, p.E, r0, lane);
+            } else {
+                if (tid == 0) found[0] = -1;
+                __syncthreads();
+                for (int j = tid; j < p.E; j += 256) {
+                    const uint32_t mine = key(t0, j);
+                    int rank = 0;
+                    for (int i = 0; i < p.E; ++i) {
+                        const uint32_t k = key(t0, i);
+                        rank += k > mine || (k == mine && i < j);
+                    }
+                    if (rank == r0 && mine > kMoeNone) found[0] = j;
+                }
+                __syncthreads();
+                e = found[0];
+            }
+        }
+        // the tokens that chose it
+        for (int t = wave; t < p.T; t += 4) {
+            const int rank = e < 0 ? kMoeMaxExperts
+                                   : moe_rank([&](int j) { return key(t, j); }, p.E, e, lane);
+            if (lane == 0) ranks[t] = rank < p.topk ? rank : -1;
         }
         __syncthreads();
-        e = found[0];
+        if (wave == 0) {
+            const int rank = lane < p.T ? ranks[lane] : -1;
+            const uint64_t m = __ballot(rank >= 0);
+            if (rank >= 0) list[__popcll(m & ((1ull << lane) - 1))] = lane * p.topk + rank;
+            // an expert that an earlier token chose is that token's slot
+            if (lane == 0)
+                found[1] = own && (m & ((1ull << t0) - 1)) ? 0 : (int)__popcll(m);
+        }
+        __syncthreads();
+        n = uniform(found[1]);
+        e = uniform(e);
     }
-    // its tokens
-    for (int t = wave; t < p.T; t += 4) {
-        const float *l = p.logits + (int64_t)t * p.ldl;
-        const uint32_t mine = moe_key(l[e]);
-        const int rank = moe_rank(l, p.E, e, mine, lane);
-        if (lane == 0) ranks[t] = rank < p.topk && mine > kMoeNone ? rank : -1;
-    }
-    __syncthreads();
-    if (wave == 0) {
-        const int rank = lane < p.T ? ranks[lane] : -1;
-        const uint64_t m = __ballot(rank >= 0);
-        if (rank >= 0) list[__popcll(m & ((1ull << lane) - 1))] = lane * p.topk + rank;
-        // an expert that an earlier token chose is that token's slot
-        if (lane == 0) found[1] = (m & ((1ull << t0) - 1)) ? 0 : (int)__popcll(m);
-    }
-    __syncthreads();
-    const int n = found[1];
     if (blockIdx.x == gridDim.x - 1) {
         if (tid == 0) p.count[slot] = n, p.expert[slot] = e;
         if (tid < n) p.pairs[slot * p.T + tid] = list[tid];
@@ -193,138 +263,194 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
     }
     if (n == 0) return;
 
-    const int r = lane & 15;
-    const uint8_t *xr[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)  // rows past the last token repeat it; not stored
-        xr[t] = p.X + (int64_t)(list[min(16 * t + r, n - 1)] / p.topk) * p.ldx * 2;
-    const int blocks = (p.H + S::KB - 1) / S::KB, per = (blocks + 3) / 4;
-    const int bbeg = min(wave * per, blocks), bend = min((wave + 1) * per, blocks);
+    const int groups = (p.H + S::KG - 1) / S::KG, per = (groups + 3) / 4;
+    const int gbeg = min(wave * per, groups), gend = min((wave + 1) * per, groups);
     const int64_t first = (int64_t)e * 2 * p.I;
+    auto token = [&](int i) {  // rows past the last token repeat it; not stored
+        return (uint32_t)(list[min(i, n - 1)] / p.topk) * (uint32_t)p.ldx * 2u;
+    };
+#pragma nounroll
     for (int jb = blockIdx.x; jb * 16 < p.I; jb += gridDim.x - 1) {
-        const int j = min(jb * 16 + r, p.I - 1);
-        const uint8_t *wr[2] = {p.W1 + (first + j) * p.ld1 * S::WES,
-                                p.W1 + (first + p.I + j) * p.ld1 * S::WES};
-        f32x4 acc[MT][2] = {};
-        Stream<IT, W8, MT, 2, U, VEC, VEC> stream;
-        stream.run(wr, xr, lane, bbeg, bend, p.H, acc);
+        const int lane = opaque(tid & 63);
+        StreamRows w[2];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            sums[wave][2 * t][lane] = acc[t][0];
-            sums[wave][2 * t + 1][lane] = acc[t][1];
-        }
-        __syncthreads();
-        // lane: row 16 t + lane % 16, four columns from 4 (lane / 16)
-        if (wave < MT) {
-            const int t = wave, row = 16 * t + r, c = jb * 16 + 4 * (lane >> 4);
-            f32x4 g = sums[0][2 * t][lane], u = sums[0][2 * t + 1][lane];
+        for (int f = 0; f < 2; ++f)
+            w[f].set(lane, p.W1 + (first + f * p.I + jb * 16) * p.ld1 * S::WES, [&](int i) {
+                return (uint32_t)min(i, p.I - 1 - jb * 16) * (uint32_t)p.ld1 * S::WES;
+            });
+#pragma nounroll
+        for (int n0 = 0; n0 < n; n0 += ROWS) {
+            int tiles = 1;
+            const int lane = opaque(tid & 63);
+            bool few_rows = true;
+            if constexpr (MT > 0) few_rows = n - n0 <= 4;
+            if (few_rows) {
+                StreamFew<IT, W8, 2, VEC, VEC> few;
+                few.run(w, p.X, token(n0 + ((lane & 15) >> 2)), lane, gbeg, gend, p.H);
+                Unroll<0, 2>::run([&](auto ff) {
+                    constexpr int f = decltype(ff)::value;
+                    const f32x4 v = few.template sums<f>(lane);
+                    if ((lane & 3) == 0) sums[wave][f][(lane & 48) | ((lane & 15) >> 2)] = v;
+                });
+            } else if (MT > 0 && (MT == 1 || n - n0 <= 16)) {
+                StreamRows x[1];
+                x[0].set(lane, p.X, [&](int i) { return token(n0 + i); });
+                f32x4 acc[1][2] = {};
+                Stream<IT, W8, 1, 2, false, VEC, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.H, acc);
+                sums[wave][0][lane] = acc[0][0];
+                sums[wave][1][lane] = acc[0][1];
+            } else if constexpr (MT == 2) {
+                tiles = 2;
+                StreamRows x[2];
 #pragma unroll
-            for (int z = 1; z < 4; ++z) {
+                for (int t = 0; t < 2; ++t)
+                    x[t].set(lane, p.X, [&](int i) { return token(n0 + 16 * t + i); });
+                f32x4 acc[2][2] = {};
+                Stream<IT, W8, 2, 2, false, VEC, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.H, acc);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    g[q] += sums[z][2 * t][lane][q];
-                    u[q] += sums[z][2 * t + 1][lane][q];
-                }
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) sums[wave][2 * t + f][lane] = acc[t][f];
             }
-            if (row < n && c < p.I) {
+            __syncthreads();
+            // lane: row 16 t + lane % 16, four columns from 4 (lane / 16)
+            if (wave < tiles) {
+                const int t = wave, row = n0 + 16 * t + (lane & 15);
+                const int c = jb * 16 + 4 * (lane >> 4);
+                if (row < n && c < p.I) {
+                    f32x4 g = sums[0][2 * t][lane], u = sums[0][2 * t + 1][lane];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (W8) {
-                        const int cq = min(c + q, p.I - 1);
-                        g[q] *= p.s1[first + cq];
-                        u[q] *= p.s1[first + p.I + cq];
+                    for (int z = 1; z < 4; ++z) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            g[q] += sums[z][2 * t][lane][q];
+                            u[q] += sums[z][2 * t + 1][lane][q];
+                        }
                     }
-                    g[q] = moe_activate(g[q], p.act) * u[q];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (W8) {
+                            const int cq = min(c + q, p.I - 1);
+                            g[q] *= p.s1[first + cq];
+                            u[q] *= p.s1[first + p.I + cq];
+                        }
+                        g[q] = moe_activate(g[q], p.act) * u[q];
+                    }
+                    // h is rounded to x's type: the second product's operand has
+                    // to be of that type, and its rounding errors, of independent
+                    // signs, come to about as much as y's own
+                    moe_store4<IT>(p.h + (int64_t)list[row] * p.ldh * 2, c, p.I - c, true, g);
                 }
-                // h is rounded to x's type: the second product's operand has
-                // to be of that type, and its rounding errors, of independent
-                // signs, come to about as much as y's own
-                moe_store4<IT>(p.h + (int64_t)list[row] * p.ldh * 2, c, p.I - c, true, g);
             }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
-// Workgroup b computes columns [16 b, 16 b + 16) of y.  Eight waves share the
+// Workgroup b computes columns [16 b, 16 b + 16) of y.  W waves share the
 // (expert, part of I) units; each adds w * (h D_e^T) to its own copy of y in LDS
-// (16 columns of every token), and the copies are added in order.
-template <int IT, bool W8, int MT, bool VEC>
-__global__ void __launch_bounds__(512) moe_down_kernel(MoeParams p) {
+// (16 columns of every token), and the copies are added in order.  TM: the most
+// tokens.
+template <int IT, bool W8, int TM, int W, bool VEC>
+__global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
-    constexpr int W = 8;
-    constexpr int U = MT == 4 ? 2 : (W8 ? 2 : 4);
-    __shared__ f32x4 y[W][16 * MT][4];
-    __shared__ int slot_of[kMoeMaxExperts], begin[kMoeMaxExperts + 1], active;
-    __shared__ int pairs[kMoeMaxTokens * kMoeMaxTopk];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n0 = blockIdx.x * 16, r = lane & 15, lg = lane >> 4;
+    constexpr int MT = TM <= 4 ? 0 : (TM <= 16 ? 1 : 2), ROWS = MT == 0 ? 4 : 16 * MT;
+    __shared__ f32x4 y[W][TM][4];
+    __shared__ int active[kMoeMaxExperts], count[kMoeMaxExperts], expert[kMoeMaxExperts], found;
+    __shared__ int pairs[kMoeStaged];
+    __shared__ float weight[kMoeMaxTokens * kMoeMaxTopk];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int n0 = blockIdx.x * 16;
+    const bool staged = p.slots * p.T <= kMoeStaged;
 
-    for (int i = tid; i < W * 16 * MT * 4; i += 64 * W)
-        (&y[0][0][0])[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // the slots that have tokens, and where their pairs start
-    if (wave == 0) {
-        int a = 0, at = 0;
+    // everything that the first kernel found, in one go
+    for (int i = tid; i < p.slots; i += 64 * W) {
+        count[i] = p.count[i];
+        expert[i] = p.expert[i];
+    }
+    if (staged)
+        for (int i = tid; i < p.slots * p.T; i += 64 * W) pairs[i] = p.pairs[i];
+    for (int i = tid; i < p.T * p.topk; i += 64 * W) weight[i] = p.weight[i];
+    if (wave == 0) {  // the slots that have tokens
+        int a = 0;
         for (int s0 = 0; s0 < p.slots; s0 += 64) {
-            const int s = s0 + lane, c = s < p.slots ? p.count[s] : 0;
-            const uint64_t m = __ballot(c > 0);
-            int sum = c;  // inclusive prefix sum over the wave
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(sum, d);
-                if (lane >= d) sum += o;
-            }
-            if (c > 0) {
-                const int pos = a + __popcll(m & ((1ull << lane) - 1));
-                slot_of[pos] = s;
-                begin[pos] = at + sum - c;
-            }
+            const int s = s0 + lane;
+            const bool any = s < p.slots && p.count[s] > 0;
+            const uint64_t m = __ballot(any);
+            if (any) active[a + __popcll(m & ((1ull << lane) - 1))] = s;
             a += __popcll(m);
-            at += __shfl(sum, 63);
         }
-        if (lane == 0) active = a, begin[a] = at;
+        if (lane == 0) found = a;
     }
-    __syncthreads();
-    const int A = active;
-    for (int a = wave; a < A; a += W) {
-        const int b0 = begin[a], c = begin[a + 1] - b0;
-        if (lane < c) pairs[b0 + lane] = p.pairs[slot_of[a] * p.T + lane];
-    }
+    for (int i = tid; i < W * TM * 4; i += 64 * W)
+        (&y[0][0][0])[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
 
     // parts of I for each expert: enough units for every wave, evenly
-    const int blocks = (p.I + S::KB - 1) / S::KB;
+    const int A = uniform(found);
+    const int groups = (p.I + S::KG - 1) / S::KG;
     int parts = 1;
     while (parts < W && (A * parts) % W != 0 && A * parts < 4 * W) ++parts;
-    const int per = (blocks + parts - 1) / parts;
+    const int per = (groups + parts - 1) / parts;
     for (int unit = wave; unit < A * parts; unit += W) {
-        const int a = unit / parts, z = unit % parts;
-        const int b0 = begin[a], n = begin[a + 1] - b0, e = p.expert[slot_of[a]];
-        const int j = min(n0 + r, p.H - 1);
-        const uint8_t *wr[1] = {p.W2 + ((int64_t)e * p.H + j) * p.ld2 * S::WES};
-        const uint8_t *xr[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            xr[t] = p.h + (int64_t)pairs[b0 + min(16 * t + r, n - 1)] * p.ldh * 2;
-        f32x4 acc[MT][1] = {};
-        Stream<IT, W8, MT, 1, U, true, VEC> stream;
-        stream.run(wr, xr, lane, min(z * per, blocks), min((z + 1) * per, blocks), p.I, acc);
+        const int lane = opaque(tid & 63), lg = lane >> 4;
+        const int slot = uniform(active[unit / parts]), z = unit % parts;
+        const int n = uniform(count[slot]), e = uniform(expert[slot]);
+        const int gbeg = min(z * per, groups), gend = min((z + 1) * per, groups);
+        auto pair = [&](int i) {
+            const int at = slot * p.T + min(i, n - 1);
+            if (staged) return pairs[at];
+            return p.pairs[at];
+        };
+        auto hrow = [&](int i) { return (uint32_t)pair(i) * (uint32_t)p.ldh * 2u; };
+        StreamRows w[1];
+        w[0].set(lane, p.W2 + ((int64_t)e * p.H + n0) * p.ld2 * S::WES, [&](int i) {
+            return (uint32_t)min(i, p.H - 1 - n0) * (uint32_t)p.ld2 * S::WES;
+        });
         f32x4 s = {1.0f, 1.0f, 1.0f, 1.0f};
         if constexpr (W8) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 s[q] = p.s2[(int64_t)e * p.H + min(n0 + 4 * lg + q, p.H - 1)];
         }
+        // add row i's sums v of columns 4 lg + 0 .. 3
+        auto add = [&](int i, const f32x4 &v) {
+            const int at = pair(i);
+            const float wt = weight[at];
+            f32x4 *dst = &y[wave][at / p.topk][lg];
+            f32x4 o = *dst;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int row = 16 * t + r;
-            if (row < n) {
-                const int pair = pairs[b0 + row];
-                const float w = p.weight[pair];
-                f32x4 *dst = &y[wave][pair / p.topk][lg];
-                f32x4 v = *dst;
+            for (int q = 0; q < 4; ++q) o[q] += wt * (v[q] * s[q]);
+            *dst = o;
+        };
+#pragma nounroll
+        for (int i0 = 0; i0 < n; i0 += ROWS) {
+            const int lane = opaque(tid & 63), r = lane & 15;
+            if (MT == 0 || n - i0 <= 4) {
+                StreamFew<IT, W8, 1, true, VEC> few;
+                few.run(w, p.h, hrow(i0 + (r >> 2)), lane, gbeg, gend, p.I);
+                const f32x4 v = few.template sums<0>(lane);
+                if ((lane & 3) == 0 && i0 + (r >> 2) < n) add(i0 + (r >> 2), v);
+            } else if (MT > 0 && (MT == 1 || n - i0 <= 16)) {
+                StreamRows x[1];
+                x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); });
+                f32x4 acc[1][1] = {};
+                Stream<IT, W8, 1, 1, false, true, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.I, acc);
+                if (i0 + r < n) add(i0 + r, acc[0][0]);
+            } else if constexpr (MT == 2) {
+                StreamRows x[2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += w * (acc[t][0][q] * s[q]);
-                *dst = v;
+                for (int t = 0; t < 2; ++t)
+                    x[t].set(lane, p.h, [&](int i) { return hrow(i0 + 16 * t + i); });
+                f32x4 acc[2][1] = {};
+                Stream<IT, W8, 2, 1, false, true, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.I, acc);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (i0 + 16 * t + r < n) add(i0 + 16 * t + r, acc[t][0]);
             }
         }
     }
@@ -341,8 +467,8 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeParams p) {
         // a token whose weights are NaN has a NaN row, also where no expert was
         // chosen
         for (int k = 0; k < p.topk; ++k) {
-            const float w = p.weight[t * p.topk + k];
-            if (w != w) v = f32x4{w, w, w, w};
+            const float wt = weight[t * p.topk + k];
+            if (wt != wt) v = f32x4{wt, wt, wt, wt};
         }
         uint8_t *row = p.D + (int64_t)t * p.ldd * 2;
         const bool vec = (reinterpret_cast<uintptr_t>(p.D) % 8 == 0) && p.ldd % 4 == 0;
@@ -356,15 +482,15 @@ hipError_t moe_launch(const MoeParams &p, int up_blocks, hipStream_t s) {
     void *args[] = {&arg};
     const dim3 up((unsigned)up_blocks + 1, (unsigned)p.slots), down((unsigned)((p.H + 15) / 16));
     const void *k1, *k2;
-    if (p.T <= 16) {
+    if (p.T <= 4) {
+        k1 = (const void *)moe_up_kernel<IT, W8, 0, VEC>;
+        k2 = (const void *)moe_down_kernel<IT, W8, 4, 8, VEC>;
+    } else if (p.T <= 16) {
         k1 = (const void *)moe_up_kernel<IT, W8, 1, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 1, VEC>;
-    } else if (p.T <= 32) {
-        k1 = (const void *)moe_up_kernel<IT, W8, 2, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 2, VEC>;
+        k2 = (const void *)moe_down_kernel<IT, W8, 16, 8, VEC>;
     } else {
-        k1 = (const void *)moe_up_kernel<IT, W8, 4, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 4, VEC>;
+        k1 = (const void *)moe_up_kernel<IT, W8, 2, VEC>;
+        k2 = (const void *)moe_down_kernel<IT, W8, 64, 8, VEC>;
     }
     const hipError_t st = hipLaunchKernel(k1, up, dim3(256), args, 0, s);
     if (st != hipSuccess) return st;

@@ -98,7 +98,8 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
     p.cd_vec = (uintptr_t)D % (4 * osz) == 0 && ldd % 4 == 0;
 
     const int akc = layoutA == GEMM_ROW_MAJOR, bkc = layoutB == GEMM_COL_MAJOR;
-    if (M <= 64 && akc && bkc && aligned)
+    // (row offsets of the streaming kernels are 32 bits: 64 rows of A, 32 of B)
+    if (M <= 64 && akc && bkc && aligned && lda <= (1 << 25) && ldb <= (1 << 25))
         return launch_scaled_stream(p, topo.cus, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     // the int8 shape classes of gemm_run (without its split along K)
     int bm, bk;

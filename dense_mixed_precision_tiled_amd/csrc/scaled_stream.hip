@@ -8,33 +8,51 @@
 namespace libgemm {
 
 // Workgroup b computes columns [16 NF b, 16 NF (b + 1)) of D for all rows; its
-// W waves split K.
-template <int MT, int NF, int W, int U>
+// W waves split K.  MT: groups of 16 rows, or 0 for at most four rows.
+template <int MT, int NF, int W, bool DB>
 __global__ void __launch_bounds__(64 * W) scaled_stream_kernel(Params p) {
     using S = StreamTypes<IT_I8, false>;
-    __shared__ f32x4 part[W][MT * NF][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int TILES = MT == 0 ? 1 : MT;
+    __shared__ f32x4 part[W][TILES * NF][64];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * NF, r = lane & 15;
     const uint8_t *A = reinterpret_cast<const uint8_t *>(p.A);
     const uint8_t *B = reinterpret_cast<const uint8_t *>(p.B);
     // rows past M and channels past N repeat the last one: their sums are not
     // stored
-    const uint8_t *wr[NF], *xr[MT];
+    StreamRows w[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) wr[f] = B + (int64_t)min(n0 + 16 * f + r, p.N - 1) * p.ldb;
+    for (int f = 0; f < NF; ++f)
+        w[f].set(lane, B + (int64_t)n0 * p.ldb,
+                 [&](int i) { return (uint32_t)(min(16 * f + i, p.N - 1 - n0) * (int)p.ldb); });
+    const int groups = (p.K + S::KG - 1) / S::KG, per = (groups + W - 1) / W;
+    const int gbeg = min(wave * per, groups), gend = min((wave + 1) * per, groups);
+    if constexpr (MT == 0) {  // at most four rows
+        StreamFew<IT_I8, false, NF, true, true> stream;
+        stream.run(w, A, (uint32_t)(min(r >> 2, p.M - 1) * (int)p.lda), lane, gbeg, gend, p.K);
+        Unroll<0, NF>::run([&](auto ff) {
+            constexpr int f = decltype(ff)::value;
+            const f32x4 v = stream.template sums<f>(lane);
+            if ((lane & 3) == 0) part[wave][f][(lane & 48) | (r >> 2)] = v;
+        });
+    } else {
+        StreamRows x[TILES];
+        f32x4 acc[TILES][NF] = {};  // int32 sums
 #pragma unroll
-    for (int t = 0; t < MT; ++t) xr[t] = A + (int64_t)min(16 * t + r, p.M - 1) * p.lda;
-    f32x4 acc[MT][NF] = {};  // int32 sums
-    const int blocks = (p.K + S::KB - 1) / S::KB, per = (blocks + W - 1) / W;
-    Stream<IT_I8, false, MT, NF, U, true, true> stream;
-    stream.run(wr, xr, lane, min(wave * per, blocks), min((wave + 1) * per, blocks), p.K, acc);
+        for (int t = 0; t < TILES; ++t)
+            x[t].set(lane, A, [&](int i) {
+                return (uint32_t)min(16 * t + i, p.M - 1) * (uint32_t)p.lda;
+            });
+        Stream<IT_I8, false, TILES, NF, DB, true, true> stream;
+        stream.run(w, x, lane, gbeg, gend, p.K, acc);
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) part[wave][t * NF + f][lane] = acc[t][f];
+            for (int f = 0; f < NF; ++f) part[wave][t * NF + f][lane] = acc[t][f];
+    }
     __syncthreads();
     // tile (t, f): lane holds row 16 t + lane % 16, four columns from 4 (lane / 16)
-    for (int tile = wave; tile < MT * NF; tile += W) {
+    for (int tile = wave; tile < TILES * NF; tile += W) {
         i32x4 n = {0, 0, 0, 0};
 #pragma unroll
         for (int z = 0; z < W; ++z) n += __builtin_bit_cast(i32x4, part[z][tile][lane]);
@@ -63,33 +81,37 @@ __global__ void __launch_bounds__(64 * W) scaled_stream_kernel(Params p) {
     }
 }
 
-template <int MT, int NF, int W, int U>
+template <int MT, int NF, int W, bool DB>
 static hipError_t launch_stream(const Params &p, hipStream_t s) {
     const dim3 grid((unsigned)((p.N + 16 * NF - 1) / (16 * NF)));
-    return launch_params(scaled_stream_kernel<MT, NF, W, U>, grid, dim3(64 * W), p, s);
+    return launch_params(scaled_stream_kernel<MT, NF, W, DB>, grid, dim3(64 * W), p, s);
 }
 
-// Variants, measured with the weights in memory (us; M x N x K):
-//                    1x4096x4096  1x4096x16384  1x16384x4096  16x16384x16384
-//   NF 1, 8 waves, U 2    6.3         14.3          15.2          65.4
-//   NF 1, 4 waves, U 4    6.2         16.3          13.9          63.4
-//   NF 2, 4 waves, U 4    7.6         19.8          14.5          60.1
-// One workgroup for 16 channels; eight waves where that leaves few workgroups
-// (more loads in flight on each CU); two channel groups for each wave where
-// x is long enough that reading it for every 16 channels counts.  With more row
-// groups x's reads count for more: at 32 rows NF 4 takes 17.5 us for
-// 32x16384x4096 where NF 1 takes 25.7, but 15.4 against 9.0 for 32x4096x4096,
-// where it leaves 64 workgroups.
+// Variants, measured with the weights in memory (us):
+//   M x N x K             16x8  16x4  32x4      (channels x waves of a workgroup)
+//   1 x 4096 x 4096       6.1   6.2   6.7       at most four rows
+//   1 x 4096 x 16384     14.0  16.1  17.5
+//   1 x 16384 x 4096     14.9  14.4  14.6
+//   16 x 16384 x 16384   49.1  53.5  56.1       one group of 16 rows
+//   1 x 16384 x 4096     16.7  14.6  14.5       (the same for one row)
+//   32 x 4096 x 4096      7.9   7.8  10.8       two groups
+//   32 x 16384 x 4096    21.0  21.2  17.5
+//   64 x 4096 x 16384    23.9  26.0  33.0       four groups
+//   64 x 16384 x 4096    28.0  27.1  20.7
+// More waves where each still has a few groups of K to load ahead (or there are
+// few workgroups); with several row groups the reads of x weigh as much as those
+// of the weights, and 32 channels halve them once that leaves a workgroup for
+// every CU.
 hipError_t launch_scaled_stream(const Params &p, int cus, hipStream_t s) {
     if (p.M > 64 || p.K <= 0) return hipErrorInvalidValue;
-    const bool few = p.N <= 32 * cus;
-    if (p.M <= 16) {
-        if (few) return launch_stream<1, 1, 8, 2>(p, s);
-        if ((int64_t)p.M * p.K >= 131072) return launch_stream<1, 2, 4, 4>(p, s);
-        return launch_stream<1, 1, 4, 4>(p, s);
-    }
-    if (p.M <= 32) return few ? launch_stream<2, 1, 4, 4>(p, s) : launch_stream<2, 4, 4, 2>(p, s);
-    return few ? launch_stream<4, 1, 4, 2>(p, s) : launch_stream<4, 4, 8, 1>(p, s);
+    const bool many = p.N >= 32 * cus;
+    if (p.M <= 4) return launch_stream<0, 1, 8, true>(p, s);
+    if (p.M <= 16)
+        return many && p.K < 8192 ? launch_stream<1, 1, 4, true>(p, s)
+                                  : launch_stream<1, 1, 8, true>(p, s);
+    if (p.M <= 32)
+        return many ? launch_stream<2, 2, 4, false>(p, s) : launch_stream<2, 1, 4, true>(p, s);
+    return many ? launch_stream<4, 2, 4, false>(p, s) : launch_stream<4, 1, 8, false>(p, s);
 }
 
 }  // namespace libgemm

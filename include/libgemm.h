@@ -438,7 +438,7 @@ int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
  *
  * gemm_moe_t describes the layer:
  *   H, I, E, topk   model width, inner width, experts (<= 1024), experts of a
- *                token (<= 32, <= E); H, I in [1, 2^24]
+ *                token (<= 32, <= E); H, I in [1, 2^19]
  *   w_dtype      GEMM_F16 or GEMM_BF16 (then the type of x), or GEMM_I8
  *   W1, ld1      E x 2I rows of H elements, lines ld1 >= H elements apart: rows
  *                [0, I) of an expert are its gate G, rows [I, 2I) its up U
@@ -473,7 +473,8 @@ int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
  *
  * Errors: GEMM_ERR_INVALID_DIM (T < 0; H, I, E or topk out of range above or
  * topk > E), GEMM_ERR_UNSUPPORTED (T > 64, E > 1024, topk > 32, a dtype or
- * activation not named above), GEMM_ERR_INVALID_LD, GEMM_ERR_NULL_PTR,
+ * activation not named above), GEMM_ERR_INVALID_LD (a line shorter than its
+ * row, or longer than 2^24 elements), GEMM_ERR_NULL_PTR,
  * GEMM_ERR_ALIASING (D or the workspace overlapping another argument),
  * GEMM_ERR_SCRATCH_TOO_SMALL, GEMM_ERR_HIP (D is then not written).
  */

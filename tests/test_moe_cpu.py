@@ -34,13 +34,14 @@ def test_accepts():
 def test_refuses():
     assert check(T=-1) == -1 and check(H=0) == -1 and check(I=0) == -1
     assert check(E=0) == -1 and check(topk=0) == -1 and check(topk=9) == -1
-    assert check(H=2 ** 24 + 1) == -1
+    assert check(H=2 ** 19 + 1) == -1 and check(I=2 ** 19 + 1) == -1
     assert check(T=65) == -4 and check(E=1025, ldl=1025) == -4
     assert check(E=64, topk=33, ldl=64) == -4
     assert check(i=lg.GEMM_F32) == -4 and check(i=F16) == -4      # bf16 weights
     assert check(w=lg.GEMM_FP8_E4M3) == -4 and check(act=lg.GEMM_ACT_NONE) == -4
     assert check(ldx=63) == -2 and check(ldl=7) == -2 and check(ldd=63) == -2
     assert check(ld1=63) == -2 and check(ld2=31) == -2
+    assert check(ldx=2 ** 24 + 1) == -2 and check(ld1=2 ** 24) == 0
     for name in ("X", "l", "D", "ws"):
         assert check(**{name: None}) == -3, name
     assert check(W1=0) == -3 and check(W2=0) == -3
