@@ -57,7 +57,7 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_I8 = 3, DT_I32 = 4 };
 // input (A, B) element types of the kernels: fp16, bf16, int8, OCP fp8 E4M3, E5M2;
 // IT_I8S: int8 whose int32 sums are scaled by row and column into a float
-// output (scaled_epilogue)
+// output (ScaledEpilogue)
 enum { IT_F16 = 0, IT_BF16 = 1, IT_I8 = 2, IT_FP8 = 3, IT_BF8 = 4, IT_I8S = 5 };
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
@@ -1877,108 +1877,278 @@ __device__ __forceinline__ void tile_epilogue(const Params &p,
     }
 }
 
+// Two fp32 values as 16-bit outputs (RNE, NaN stays NaN) in one dword, by the
+// conversion instructions.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack_out16(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v = {lo, hi};
+    if constexpr (OUT == DT_F16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// gelu_f32 with its infinities selected rather than branched on, for unrolled
+// code: at +Inf the formula gives Inf * 1 by itself, at -Inf it would be Inf * 0.
+__device__ __forceinline__ float gelu_select(float x) {
+    const float z = __builtin_fabsf(x) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * z);
+    const float poly =
+        t * (0.254829592f +
+             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float q = 0.5f * poly * __expf(-z * z);
+    const float y = x * (x >= 0.0f ? 1.0f - q : q);
+    return x == -__builtin_inff() ? 0.0f : y;
+}
+
 // The epilogue of the scaled int8 products (IT_I8S, float outputs):
 //   D(i,j) = act(alpha * (n * row_scale[i] * col_scale[j]) + beta * C + bias)
 // with n the exact int32 sum, rounded to fp32 first (relative 2^-24).  The row
 // scale is applied before the column scale: their product alone could leave
 // the range of fp32.
-// Every tile is staged through LDS, one MF-row block per wave at a time, and
-// finished in a loop that is not unrolled: a lane then owns the same four
-// columns of every row it finishes, so the columns' scales and bias are eight
-// registers for the whole tile, and a wave stores whole row segments (256
-// bytes of 16-bit outputs at 128 columns) instead of 8 bytes in each of 16
-// rows.  (In registers, as tile_epilogue finishes interior tiles, the scales
-// of a lane's rows and columns and the three output types made the eight-wave
-// kernels spill 100 to 550 registers.)  Row values are staged in LDS as well: a
-// load from memory between two stores waits for both.
+// Every tile is staged through LDS, one MF-row block per wave at a time: a lane
+// then owns the same columns of every row it finishes, so the columns' scales and
+// bias are a few registers for the whole tile, and a wave stores whole row
+// segments (256 bytes of 16-bit outputs at 128 columns) instead of 8 bytes in
+// each of 16 rows.  (In registers, as tile_epilogue finishes interior tiles, the
+// scales of a lane's rows and columns and the three output types made the
+// eight-wave kernels spill 100 to 550 registers.)  Row values are staged in LDS
+// as well: a load from memory between two stores waits for both.
+//
+// Without C and activation the blocks are unrolled, over two LDS buffers where
+// they fit, block i + 1 written before block i is read: with one wave on each SIMD
+// nothing else hides the LDS latency.  There a lane owns four consecutive columns where
+// D takes vector stores, and single columns 64 apart otherwise (a store of
+// consecutive elements, whatever D's alignment).  C, an activation and satf take a
+// loop over the blocks that is not unrolled, so their arithmetic is instantiated
+// once.
 template <class CF, int SMEM_BYTES, bool AGPR>
-__device__ __forceinline__ void scaled_epilogue(
-    const Params &p, typename AccT<CF::MF>::type (&acc)[CF::TM][CF::TN], int m0, int n0,
-    u32x4 *smem, int tid) {
-    constexpr int MF = CF::MF, TM = CF::TM, TN = CF::TN, WTN = CF::WTN;
-    constexpr int NG = AccT<MF>::N / 4;
-    constexpr int SROW = WTN + 8;  // words per staged row, padded against bank conflicts
-    constexpr int LPR = WTN / 4, RPP = 64 / LPR;
-    constexpr int WAVES = CF::WAVES_M * CF::WAVES_N;
-    static_assert(64 % LPR == 0 && MF % RPP == 0, "lanes per staged row");
-    static_assert((WAVES * MF * SROW + 2 * WAVES * CF::WTM) * 4 <= SMEM_BYTES,
-                  "staging fits in the operand buffers");
-    const int lane = tid & 63, wave = tid >> 6;
-    const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
-    float *const stage = reinterpret_cast<float *>(smem) + wave * MF * SROW;
-    float *const rows = reinterpret_cast<float *>(smem) + WAVES * MF * SROW + wave * 2 * CF::WTM;
-    const int row0 = m0 + wm * CF::WTM;
-    const int c4 = (lane % LPR) * 4, gj = n0 + wn * WTN + c4;
-    for (int r = lane; r < CF::WTM; r += 64) {
-        const int gi = min(row0 + r, p.M - 1);
-        rows[r] = p.row_scale ? p.row_scale[gi] : 1.0f;
-        rows[CF::WTM + r] = (p.bias && p.bias_rows) ? p.bias[gi] : 0.0f;
+struct ScaledEpilogue {
+    static constexpr int MF = CF::MF, TM = CF::TM, TN = CF::TN, WTM = CF::WTM, WTN = CF::WTN;
+    static constexpr int NG = AccT<MF>::N / 4;
+    static constexpr int SROW = WTN + 8;  // words per staged row, padded against bank conflicts
+    static constexpr int WAVES = CF::WAVES_M * CF::WAVES_N;
+    // two staged blocks for each wave where they fit, else one
+    static constexpr int BUFS = (WAVES * 2 * MF * SROW + 2 * WAVES * WTM) * 4 <= SMEM_BYTES ? 2 : 1;
+    static constexpr int ROWS0 = WAVES * BUFS * MF * SROW;  // words of the staged blocks
+    static_assert((ROWS0 + 2 * WAVES * WTM) * 4 <= SMEM_BYTES, "fits in the operand buffers");
+    using Acc = typename AccT<MF>::type;
+
+    const Params &p;
+    float *stage, *rows;  // this wave's blocks; its rows' scales, then biases
+    int lane, row0, col0;
+
+    __device__ __forceinline__ ScaledEpilogue(const Params &p_, int m0, int n0, u32x4 *smem,
+                                              int tid)
+        : p(p_) {
+        lane = tid & 63;
+        const int wave = tid >> 6;
+        stage = reinterpret_cast<float *>(smem) + wave * BUFS * MF * SROW;
+        rows = reinterpret_cast<float *>(smem) + ROWS0 + wave * 2 * WTM;
+        row0 = m0 + wave / CF::WAVES_N * WTM;
+        col0 = n0 + wave % CF::WAVES_N * WTN;
     }
-    f32x4 scol, bcol;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int gc = min(gj + e, p.N - 1);
-        scol[e] = p.col_scale ? p.col_scale[gc] : 1.0f;
-        bcol[e] = (p.bias && !p.bias_rows) ? p.bias[gc] : 0.0f;
-    }
-    const bool gin = p.cd_vec && gj + 4 <= p.N;
-    // C(gi, gj..gj+3); what lies outside M x N is not read and not stored
-    auto load_c4 = [&](int gi) {
-        f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (gi < p.M) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (gj + e < p.N) c[e] = load_c(p, gi, gj + e);
-        }
-        return c;
-    };
-#pragma nounroll
-    for (int i = 0; i < TM; ++i) {
-        Unroll<0, TM>::run([&](auto ii) {
-            constexpr int ic = decltype(ii)::value;
-            if (ic != i) return;
-            Unroll<0, TN>::run([&](auto jj) {
-                constexpr int j = decltype(jj)::value;
-                Unroll<0, NG>::run([&](auto gg) {
-                    constexpr int g = decltype(gg)::value;
-                    *reinterpret_cast<f32x4 *>(stage + acc_row<MF>(lane) * SROW + j * MF +
-                                               acc_col<MF>(lane, g)) =
-                        acc_group<AGPR>(acc[ic][j], g);
-                });
+    template <int I>
+    __device__ __forceinline__ void put(Acc (&acc)[TM][TN], int buf) {
+        Unroll<0, TN>::run([&](auto jj) {
+            Unroll<0, NG>::run([&](auto gg) {
+                constexpr int j = decltype(jj)::value, g = decltype(gg)::value;
+                *reinterpret_cast<f32x4 *>(stage + (buf * MF + acc_row<MF>(lane)) * SROW + j * MF +
+                                           acc_col<MF>(lane, g)) = acc_group<AGPR>(acc[I][j], g);
             });
         });
-        // (LDS operations of one wave complete in order; this only keeps the
-        // compiler from moving the reads above the writes)
-        __builtin_amdgcn_wave_barrier();
-#pragma nounroll
-        for (int rr = lane / LPR; rr < MF; rr += RPP) {
-            const int gi = row0 + i * MF + rr;
-            const i32x4 n = *reinterpret_cast<const i32x4 *>(stage + rr * SROW + c4);
-            const float srow = rows[i * MF + rr], brow = rows[CF::WTM + i * MF + rr];
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = p.alpha * ((float)n[e] * srow * scol[e]) + bcol[e] + brow;
-            if (p.C) {
-                const f32x4 c = load_c4(gi);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += p.beta * c[e];
-            }
-            const bool full = gin && gi < p.M;
-            if (p.out_dtype == DT_F32) {
-                if (full) finish4<DT_F32, true, true, true>(p, gi, gj, v);
-                else finish4<DT_F32, false, true, true>(p, gi, gj, v);
-            } else if (p.out_dtype == DT_F16) {
-                if (full) finish4<DT_F16, true, true, true>(p, gi, gj, v);
-                else finish4<DT_F16, false, true, true>(p, gi, gj, v);
-            } else {
-                if (full) finish4<DT_BF16, true, true, true>(p, gi, gj, v);
-                else finish4<DT_BF16, false, true, true>(p, gi, gj, v);
-            }
-        }
-        __builtin_amdgcn_wave_barrier();
     }
-}
+    __device__ __forceinline__ float col_scale(int c) const {
+        return p.col_scale ? p.col_scale[min(c, p.N - 1)] : 1.0f;
+    }
+    __device__ __forceinline__ float col_bias(int c) const {
+        return p.bias && !p.bias_rows ? p.bias[min(c, p.N - 1)] : 0.0f;
+    }
+
+    // No C, activation or satf.  V columns for each lane and row: four consecutive ones
+    // (vector stores), or columns of its own 64 apart.
+    template <int OUT, bool VECD>
+    __device__ __forceinline__ void plain(Acc (&acc)[TM][TN]) {
+        constexpr int V = VECD ? 4 : (WTN > 64 ? WTN / 64 : 1);
+        constexpr int LPR = VECD ? WTN / 4 : (WTN < 64 ? WTN : 64);  // lanes for a row
+        constexpr int RPP = 64 / LPR, PASSES = MF / RPP;
+        constexpr int Q = PASSES < 8 ? PASSES : 8;  // passes whose LDS reads go together
+        static_assert(64 % LPR == 0 && MF % RPP == 0 && PASSES % Q == 0, "lanes per staged row");
+        const int cl = VECD ? (lane % LPR) * 4 : lane % LPR;  // first column in the wave's part
+        auto col = [&](int e) { return cl + (VECD ? e : 64 * e); };
+        float scol[V], bcol[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            scol[e] = col_scale(col0 + col(e));
+            bcol[e] = col_bias(col0 + col(e));
+        }
+        put<0>(acc, 0);
+        Unroll<0, TM>::run([&](auto ii) {
+            constexpr int i = decltype(ii)::value, buf = i % BUFS;
+            // (LDS operations of one wave complete in order; the barriers only
+            // keep the compiler from moving reads above writes)
+            __builtin_amdgcn_wave_barrier();
+            if constexpr (i + 1 < TM && BUFS == 2) put<i + 1>(acc, buf ^ 1);
+            Unroll<0, PASSES / Q>::run([&](auto bb) {
+                int32_t n[Q][V];
+                float srow[Q], brow[Q];
+                Unroll<0, Q>::run([&](auto qq) {
+                    constexpr int q = decltype(qq)::value;
+                    const int rr = lane / LPR + (decltype(bb)::value * Q + q) * RPP;
+                    const float *src = stage + (buf * MF + rr) * SROW;
+                    if constexpr (VECD) {
+                        const i32x4 v = *reinterpret_cast<const i32x4 *>(src + cl);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) n[q][e] = v[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            n[q][e] = reinterpret_cast<const int32_t *>(src)[col(e)];
+                    }
+                    srow[q] = rows[i * MF + rr];
+                    brow[q] = rows[WTM + i * MF + rr];
+                });
+                Unroll<0, Q>::run([&](auto qq) {
+                    constexpr int q = decltype(qq)::value;
+                    const int gi = row0 + i * MF + lane / LPR + (decltype(bb)::value * Q + q) * RPP;
+                    float v[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[e] = p.alpha * ((float)n[q][e] * srow[q] * scol[e]) + bcol[e] + brow[q];
+                    const int64_t off = (int64_t)gi * p.ldd + col0;
+                    if constexpr (VECD) {
+                        if (gi < p.M && col0 + cl + 4 <= p.N) {
+                            if constexpr (OUT == DT_F32)
+                                *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p.D) + off +
+                                                           cl) = f32x4{v[0], v[1], v[2], v[3]};
+                            else
+                                *reinterpret_cast<u32x2 *>(reinterpret_cast<uint16_t *>(p.D) + off +
+                                                           cl) =
+                                    u32x2{pack_out16<OUT>(v[0], v[1]), pack_out16<OUT>(v[2], v[3])};
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            if (gi >= p.M || col0 + col(e) >= p.N) continue;
+                            if constexpr (OUT == DT_F32)
+                                reinterpret_cast<float *>(p.D)[off + col(e)] = v[e];
+                            else
+                                reinterpret_cast<uint16_t *>(p.D)[off + col(e)] =
+                                    (uint16_t)pack_out16<OUT>(v[e], v[e]);
+                        }
+                    }
+                });
+            });
+            if constexpr (i + 1 < TM && BUFS == 1) {
+                __builtin_amdgcn_wave_barrier();
+                put<i + 1>(acc, 0);
+            }
+        });
+    }
+
+    // Everything else.
+    __device__ __forceinline__ void general(Acc (&acc)[TM][TN]) {
+        constexpr int LPR = WTN / 4, RPP = 64 / LPR, PASSES = MF / RPP;
+        constexpr int Q = PASSES < 4 ? PASSES : 4;  // passes that go together
+        static_assert(64 % LPR == 0 && MF % RPP == 0 && PASSES % Q == 0, "lanes per staged row");
+        const int c4 = (lane % LPR) * 4, gj = col0 + c4;
+        f32x4 scol, bcol;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            scol[e] = col_scale(gj + e);
+            bcol[e] = col_bias(gj + e);
+        }
+        const bool gin = p.cd_vec && gj + 4 <= p.N;
+#pragma nounroll
+        for (int i = 0; i < TM; ++i) {
+            Unroll<0, TM>::run([&](auto ii) {
+                if (decltype(ii)::value == i) put<decltype(ii)::value>(acc, 0);
+            });
+            __builtin_amdgcn_wave_barrier();
+#pragma nounroll
+            for (int r0 = lane / LPR; r0 < MF; r0 += Q * RPP) {
+                f32x4 v[Q];
+                Unroll<0, Q>::run([&](auto qq) {
+                    constexpr int q = decltype(qq)::value;
+                    const int rr = r0 + q * RPP, gi = row0 + i * MF + rr;
+                    const i32x4 n = *reinterpret_cast<const i32x4 *>(stage + rr * SROW + c4);
+                    const float srow = rows[i * MF + rr], brow = rows[WTM + i * MF + rr];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[q][e] = p.alpha * ((float)n[e] * srow * scol[e]) + bcol[e] + brow;
+                        if (p.C && gi < p.M && gj + e < p.N)
+                            v[q][e] += p.beta * load_c(p, gi, gj + e);
+                    }
+                });
+                if (p.act == ACT_GELU) {
+                    Unroll<0, Q>::run([&](auto qq) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[decltype(qq)::value][e] = gelu_select(v[decltype(qq)::value][e]);
+                    });
+                } else if (p.act == ACT_RELU) {
+                    Unroll<0, Q>::run([&](auto qq) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[decltype(qq)::value][e] =
+                                activate(v[decltype(qq)::value][e], ACT_RELU);
+                    });
+                }
+                Unroll<0, Q>::run([&](auto qq) {
+                    constexpr int q = decltype(qq)::value;
+                    const int gi = row0 + i * MF + r0 + q * RPP;
+                    const bool full = gin && gi < p.M;
+                    if (full && !p.satf && p.out_dtype != DT_F32) {
+                        uint16_t *d = reinterpret_cast<uint16_t *>(p.D) + (int64_t)gi * p.ldd + gj;
+                        *reinterpret_cast<u32x2 *>(d) =
+                            p.out_dtype == DT_F16
+                                ? u32x2{pack_out16<DT_F16>(v[q][0], v[q][1]),
+                                        pack_out16<DT_F16>(v[q][2], v[q][3])}
+                                : u32x2{pack_out16<DT_BF16>(v[q][0], v[q][1]),
+                                        pack_out16<DT_BF16>(v[q][2], v[q][3])};
+                    } else if (p.out_dtype == DT_F32) {
+                        if (full) finish4<DT_F32, true, false, true>(p, gi, gj, v[q]);
+                        else finish4<DT_F32, false, false, true>(p, gi, gj, v[q]);
+                    } else if (p.out_dtype == DT_F16) {
+                        if (full) finish4<DT_F16, true, false, true>(p, gi, gj, v[q]);
+                        else finish4<DT_F16, false, false, true>(p, gi, gj, v[q]);
+                    } else {
+                        if (full) finish4<DT_BF16, true, false, true>(p, gi, gj, v[q]);
+                        else finish4<DT_BF16, false, false, true>(p, gi, gj, v[q]);
+                    }
+                });
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+
+    __device__ __forceinline__ void run(Acc (&acc)[TM][TN]) {
+        for (int r = lane; r < WTM; r += 64) {
+            const int gi = min(row0 + r, p.M - 1);
+            rows[r] = p.row_scale ? p.row_scale[gi] : 1.0f;
+            rows[WTM + r] = (p.bias && p.bias_rows) ? p.bias[gi] : 0.0f;
+        }
+        if (p.C || p.act != ACT_NONE || p.satf) {
+            general(acc);
+            return;
+        }
+        // vector stores where D allows them and N ends on a group of four
+        const bool vec = p.cd_vec && p.N % 4 == 0;
+        if (p.out_dtype == DT_F32) {
+            if (vec) plain<DT_F32, true>(acc);
+            else plain<DT_F32, false>(acc);
+        } else if (p.out_dtype == DT_F16) {
+            if (vec) plain<DT_F16, true>(acc);
+            else plain<DT_F16, false>(acc);
+        } else {
+            if (vec) plain<DT_BF16, true>(acc);
+            else plain<DT_BF16, false>(acc);
+        }
+    }
+};
 
 // ------------------------------------------------------------------ kernel
 // VEC selects the vector (aligned) or the element-wise (unaligned) loads and
@@ -2011,7 +2181,7 @@ __global__ void __launch_bounds__(CF::THREADS) gemm_mfma_kernel(Params p) {
 
     k_loop<CF, IT, A_KC, B_KC, VEC, RAGGED>(p, m0, n0, kbeg, kend, acc, sA, sB, tid);
     if constexpr (IT == IT_I8S)
-        scaled_epilogue<CF, (int)sizeof(smem), false>(p, acc, m0, n0, smem, tid);
+        ScaledEpilogue<CF, (int)sizeof(smem), false>(p, m0, n0, smem, tid).run(acc);
     else
         tile_epilogue<CF, IT, VEC, (int)sizeof(smem), false, !RAGGED>(p, acc, m0, n0, smem, tid);
 }
@@ -2042,7 +2212,7 @@ __global__ void __launch_bounds__(CF::THREADS) gemm_dma_kernel(Params p) {
     dma_k_loop<CF, IT, A_KC, B_KC, RAGGED>(p, m0, n0, kbeg, kend, acc,
                                            reinterpret_cast<char *>(smem), tid);
     if constexpr (IT == IT_I8S)
-        scaled_epilogue<CF, 2 * (BM + BN) * BK * CF::ES, true>(p, acc, m0, n0, smem, tid);
+        ScaledEpilogue<CF, 2 * (BM + BN) * BK * CF::ES, true>(p, m0, n0, smem, tid).run(acc);
     else
         tile_epilogue<CF, IT, true, 2 * (BM + BN) * BK * CF::ES, true>(p, acc, m0, n0, smem, tid);
     wait_vmcnt<0>();  // the sink's loads land before the workgroup's LDS is released
