@@ -107,8 +107,10 @@ hipError_t launch_large8_i8s(const Params &, int, int, int, dim3, hipStream_t);
 hipError_t launch_medium_i8s(const Params &, int, int, int, dim3, hipStream_t);
 hipError_t launch_small_i8s(const Params &, int, int, int, dim3, hipStream_t);
 hipError_t launch_large_dma16_i8s(const Params &, int, int, int, dim3, hipStream_t);
-// the same for M <= 64, K-contiguous 16-byte aligned operands: scaled_stream.hip
+// the same for K-contiguous 16-byte aligned operands: M <= 32 (scaled_stream.hip),
+// and few tiles (scaled_pipe.hip; false: not this kernel's sizes)
 hipError_t launch_scaled_stream(const Params &, int cus, hipStream_t);
+bool launch_scaled_pipe(const Params &, int cus, hipStream_t, hipError_t *status);
 
 // fp8 entries, one translation unit per (entry, format): kernels_<entry>_f8.hip
 // (E4M3) and kernels_<entry>_bf8.hip (E5M2); the bf flag of launch_fn selects

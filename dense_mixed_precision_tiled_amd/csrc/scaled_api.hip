@@ -16,6 +16,55 @@ namespace {
 
 int flip(int layout) { return layout == GEMM_ROW_MAJOR ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR; }
 
+// One launch.  aligned: the operands' lines allow 16-byte loads.
+int run_part(Params &p, bool aligned, int akc, int bkc, int cus, int osz, hipStream_t stream) {
+    const int64_t M = p.M, N = p.N, K = p.K;
+    auto status = [](hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; };
+    // vector loads: extents, rounded up to 16 bytes, that fit a 32-bit buffer range
+    const int64_t a_ext = akc ? (M - 1) * p.lda + K : (K - 1) * p.lda + M;
+    const int64_t b_ext = bkc ? (N - 1) * p.ldb + K : (K - 1) * p.ldb + N;
+    const int64_t a_rng = (a_ext + 15) & ~(int64_t)15, b_rng = (b_ext + 15) & ~(int64_t)15;
+    const int64_t range = ((int64_t)1 << 32) - 16;
+    p.vec_ok = aligned && a_rng < range && b_rng < range;
+    p.a_bytes = p.vec_ok ? (uint32_t)a_rng : 0u;
+    p.b_bytes = p.vec_ok ? (uint32_t)b_rng : 0u;
+    // four outputs of a row in one store
+    p.cd_vec = (uintptr_t)p.D % (4 * osz) == 0 && p.ldd % 4 == 0;
+    p.group_m = 4;
+    if (akc && bkc && aligned) {
+        // (row offsets of the streaming kernels are 32 bits: 32 rows of A and B)
+        if (M <= 32 && p.lda <= (1 << 26) && p.ldb <= (1 << 26))
+            return status(launch_scaled_stream(p, cus, stream));
+        hipError_t e;
+        if (launch_scaled_pipe(p, cus, stream, &e)) return status(e);
+    }
+    // the int8 shape classes of gemm_run (without its split along K)
+    int bm, bk;
+    launch_fn launch;
+    if (cdiv(M, 256) * cdiv(N, 256) >= 3 * cus / 4) {
+        bm = 256, bk = CfgLarge8I8::BK;
+        launch = p.vec_ok && akc && bkc && K % CfgLargeDmaI8_16::BK == 0 ? launch_large_dma16_i8s
+                                                                         : launch_large8_i8s;
+    } else if (cdiv(M, 128) * cdiv(N, 128) >= cus / 2) {
+        bm = 128, bk = CfgMediumI8::BK;
+        launch = launch_medium_i8s;
+    } else {
+        bm = 64, bk = CfgSmallI8::BK;
+        launch = launch_small_i8s;
+    }
+    p.tiles_m = (int)cdiv(M, bm);
+    p.tiles_n = (int)cdiv(N, bm);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    if (tiles > 0x7fffffff) return GEMM_ERR_INVALID_DIM;
+    // the raster of gemm_run: groups of 4 tile-rows, or 2 staggered ones where
+    // each CU runs several large tiles with a short K loop
+    const bool short_multi = bm == 256 && tiles > cus && K <= 2048;
+    p.group_m = short_multi ? 2 : 4;
+    p.skew = short_multi ? 1 : 0;
+    p.k_per_split = (int)(cdiv(K > 0 ? K : 1, bk) * bk);
+    return status(launch(p, 0, akc, bkc, dim3((unsigned)tiles), stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -58,16 +107,11 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
 
     Params p{};
-    p.A = static_cast<const uint16_t *>(A);
-    p.B = static_cast<const uint16_t *>(B);
     p.C = C;
-    p.D = D;
     p.lda = lda;
     p.ldb = ldb;
     p.ldc = C ? ldc : 0;
     p.ldd = ldd;
-    p.M = (int)M;
-    p.N = (int)N;
     p.K = (int)K;
     p.out_dtype = out_dtype;
     p.satf = satf ? 1 : 0;
@@ -82,51 +126,35 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
     p.col_scale = scaleB;
     p.splits = 1;
     p.xcds = topo.xcds;
-    // vector loads: 16-byte aligned operands whose extents, rounded up to 16
-    // bytes, fit a 32-bit buffer range
-    const int64_t a_ext = layoutA == GEMM_ROW_MAJOR ? (M - 1) * lda + K : (K - 1) * lda + M;
-    const int64_t b_ext = layoutB == GEMM_ROW_MAJOR ? (K - 1) * ldb + N : (N - 1) * ldb + K;
-    const int64_t a_rng = (a_ext + 15) & ~(int64_t)15, b_rng = (b_ext + 15) & ~(int64_t)15;
-    const int64_t range = ((int64_t)1 << 32) - 16;
+    const int akc = layoutA == GEMM_ROW_MAJOR, bkc = layoutB == GEMM_COL_MAJOR;
     const bool aligned = K > 0 && (uintptr_t)A % 16 == 0 && (uintptr_t)B % 16 == 0 &&
                          lda % 16 == 0 && ldb % 16 == 0;
-    p.vec_ok = aligned && a_rng < range && b_rng < range;
-    p.a_bytes = p.vec_ok ? (uint32_t)a_rng : 0u;
-    p.b_bytes = p.vec_ok ? (uint32_t)b_rng : 0u;
-    // four outputs of a row in one store
+    // Buffer loads reach 4 GiB: K-contiguous operands past that are taken in
+    // parts, rows of D by the extent of A and columns by that of B.
+    const int64_t range = ((int64_t)1 << 32) - 16;
+    const bool parts = aligned && akc && bkc && lda <= range / 512 && ldb <= range / 512;
+    const int64_t rows = parts && (M - 1) * lda + K > range ? (range - K) / lda / 256 * 256 : M;
+    const int64_t cols = parts && (N - 1) * ldb + K > range ? (range - K) / ldb / 256 * 256 : N;
     const int osz = out_size(out_dtype);
-    p.cd_vec = (uintptr_t)D % (4 * osz) == 0 && ldd % 4 == 0;
-
-    const int akc = layoutA == GEMM_ROW_MAJOR, bkc = layoutB == GEMM_COL_MAJOR;
-    // (row offsets of the streaming kernels are 32 bits: 64 rows of A, 32 of B)
-    if (M <= 64 && akc && bkc && aligned && lda <= (1 << 25) && ldb <= (1 << 25))
-        return launch_scaled_stream(p, topo.cus, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
-    // the int8 shape classes of gemm_run (without its split along K)
-    int bm, bk;
-    launch_fn launch;
-    if (cdiv(M, 256) * cdiv(N, 256) >= 3 * topo.cus / 4) {
-        bm = 256, bk = CfgLarge8I8::BK;
-        launch = p.vec_ok && akc && bkc && K % CfgLargeDmaI8_16::BK == 0 ? launch_large_dma16_i8s
-                                                                         : launch_large8_i8s;
-    } else if (cdiv(M, 128) * cdiv(N, 128) >= topo.cus / 2) {
-        bm = 128, bk = CfgMediumI8::BK;
-        launch = launch_medium_i8s;
-    } else {
-        bm = 64, bk = CfgSmallI8::BK;
-        launch = launch_small_i8s;
+    for (int64_t i = 0; i < M; i += rows) {
+        for (int64_t j = 0; j < N; j += cols) {
+            Params q = p;
+            q.M = (int)(M - i < rows ? M - i : rows);
+            q.N = (int)(N - j < cols ? N - j : cols);
+            q.A = reinterpret_cast<const uint16_t *>(static_cast<const char *>(A) + i * lda);
+            q.B = reinterpret_cast<const uint16_t *>(static_cast<const char *>(B) + j * ldb);
+            if (C)
+                q.C = static_cast<const char *>(C) +
+                      (p.c_col ? j * p.ldc + i : i * p.ldc + j) * osz;
+            q.D = static_cast<char *>(D) + (i * ldd + j) * osz;
+            if (p.bias) q.bias = p.bias + (p.bias_rows ? i : j);
+            if (p.row_scale) q.row_scale = p.row_scale + i;
+            if (p.col_scale) q.col_scale = p.col_scale + j;
+            const int r = run_part(q, aligned, akc, bkc, topo.cus, osz, stream);
+            if (r != GEMM_OK) return r;
+        }
     }
-    p.tiles_m = (int)cdiv(M, bm);
-    p.tiles_n = (int)cdiv(N, bm);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    if (tiles > 0x7fffffff) return GEMM_ERR_INVALID_DIM;
-    // the raster of gemm_run: groups of 4 tile-rows, or 2 staggered ones where
-    // each CU runs several large tiles with a short K loop
-    const bool short_multi = bm == 256 && tiles > topo.cus && K <= 2048;
-    p.group_m = short_multi ? 2 : 4;
-    p.skew = short_multi ? 1 : 0;
-    p.k_per_split = (int)(cdiv(K > 0 ? K : 1, bk) * bk);
-    return launch(p, 0, akc, bkc, dim3((unsigned)tiles), stream) == hipSuccess ? GEMM_OK
-                                                                               : GEMM_ERR_HIP;
+    return GEMM_OK;
 }
 
 }  // extern "C"

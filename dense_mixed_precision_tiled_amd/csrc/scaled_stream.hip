@@ -1,4 +1,4 @@
-// The scaled int8 product for few rows (M <= 64): B streamed once.
+// The scaled int8 product for few rows (M <= 32): B streamed once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -87,31 +87,27 @@ static hipError_t launch_stream(const Params &p, hipStream_t s) {
     return launch_params(scaled_stream_kernel<MT, NF, W, DB>, grid, dim3(64 * W), p, s);
 }
 
-// Variants, measured with the weights in memory (us):
-//   M x N x K             16x8  16x4  32x4      (channels x waves of a workgroup)
-//   1 x 4096 x 4096       6.1   6.2   6.7       at most four rows
-//   1 x 4096 x 16384     14.0  16.1  17.5
-//   1 x 16384 x 4096     14.9  14.4  14.6
-//   16 x 16384 x 16384   49.1  53.5  56.1       one group of 16 rows
-//   1 x 16384 x 4096     16.7  14.6  14.5       (the same for one row)
-//   32 x 4096 x 4096      7.9   7.8  10.8       two groups
-//   32 x 16384 x 4096    21.0  21.2  17.5
-//   64 x 4096 x 16384    23.9  26.0  33.0       four groups
-//   64 x 16384 x 4096    28.0  27.1  20.7
-// More waves where each still has a few groups of K to load ahead (or there are
-// few workgroups); with several row groups the reads of x weigh as much as those
-// of the weights, and 32 channels halve them once that leaves a workgroup for
-// every CU.
+// Variants, measured with the weights in memory (us), by the channels and waves
+// of a workgroup:
+//   M x N x K            16, 8   16, 4   32, 4
+//   1 x 4096 x 4096       6.1     6.2     6.7    at most four rows
+//   1 x 4096 x 16384     14.0    16.1    17.5
+//   1 x 16384 x 4096     14.9    14.4    14.6
+//   16 x 16384 x 16384   49.1    53.5    56.1    one group of 16 rows
+//   1 x 16384 x 4096     16.7    14.6    14.5    (the same for one row)
+//   32 x 4096 x 4096      7.9     7.8    10.8    two groups
+//   32 x 16384 x 4096    21.0    21.2    17.5
+// Eight waves where each has a few groups of K to load ahead, or there are few
+// workgroups; with two row groups the reads of x weigh as much as those of the
+// weights, and 32 channels halve them once that leaves a workgroup for every CU.
 hipError_t launch_scaled_stream(const Params &p, int cus, hipStream_t s) {
-    if (p.M > 64 || p.K <= 0) return hipErrorInvalidValue;
+    if (p.M > 32 || p.K <= 0) return hipErrorInvalidValue;
     const bool many = p.N >= 32 * cus;
     if (p.M <= 4) return launch_stream<0, 1, 8, true>(p, s);
     if (p.M <= 16)
         return many && p.K < 8192 ? launch_stream<1, 1, 4, true>(p, s)
                                   : launch_stream<1, 1, 8, true>(p, s);
-    if (p.M <= 32)
-        return many ? launch_stream<2, 2, 4, false>(p, s) : launch_stream<2, 1, 4, true>(p, s);
-    return many ? launch_stream<4, 2, 4, false>(p, s) : launch_stream<4, 1, 8, false>(p, s);
+    return many ? launch_stream<2, 2, 4, false>(p, s) : launch_stream<2, 1, 4, true>(p, s);
 }
 
 }  // namespace libgemm

@@ -342,9 +342,10 @@ int gemm_validate_ex(int64_t M, int64_t N, int64_t K,
  *
  * An int8 product with a scale for each row of A (a token) and each column of
  * D (an output channel), and the operator that makes such an A from 16-bit or
- * 32-bit activations.  Both enqueue exactly one kernel, allocate nothing and
- * use no workspace, so they can be captured into a HIP graph, and calls on
- * different streams do not touch each other.
+ * 32-bit activations.  Both enqueue one kernel (gemm_run_scaled one for every
+ * 4 GiB of A and of B), allocate nothing and use no workspace, so they can be
+ * captured into a HIP graph, and calls on different streams do not touch each
+ * other.
  *
  * gemm_quantize_rows: for each row i of X (M x K, row-major, ldx >= K),
  *
@@ -395,11 +396,12 @@ int gemm_validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx
  * Errors as gemm_run_ex, and: another dtype combination, or K >= 2^17 ->
  * GEMM_ERR_UNSUPPORTED; D overlapping scaleA or scaleB -> GEMM_ERR_ALIASING.
  *
- * Speed: vector loads as for gemm_run.  Calls with M <= 64 rows, K-contiguous
- * operands (row-major A, column-major B) and vector loads stream B from memory
- * once, a column block for each workgroup; other calls run the int8 tiles.
- * Operands that miss the vector loads are read element by element (gemm_run
- * copies large ones into its workspace first; this call has none).
+ * Speed: vector loads as for gemm_run.  With K-contiguous operands (row-major A,
+ * column-major B) and vector loads, up to 32 rows stream B from memory once, a
+ * column block for each workgroup, and calls of few output tiles take deeply
+ * pipelined ones; other calls run the int8 tiles.  Operands that miss the
+ * vector loads are read element by element (gemm_run copies large ones into its
+ * workspace first; this call has none).
  */
 int gemm_run_scaled(int64_t M, int64_t N, int64_t K,
                     const void *A, int64_t lda, int layoutA,

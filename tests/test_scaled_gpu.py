@@ -172,6 +172,36 @@ def test_large_tiles(la, lb, K):
     Scaled(3500, 3600, K, la, lb, out=F16, bias=True, c=True, beta=0.5).check("large")
 
 
+# sizes that the pipelined kernel's tiles of 32x32 to 128x128 each take on 256 CUs,
+# with whole and ragged K-tiles, fewer K-tiles than stages, and odd edges
+@pytest.mark.parametrize("M,N", [(40, 500), (127, 4090), (250, 4090), (499, 4096), (1000, 4001)])
+@pytest.mark.parametrize("K", [16, 128, 200, 1152])
+def test_pipelined_tiles(M, N, K):
+    Scaled(M, N, K, out=BF16, bias=True).check("pipelined")
+    Scaled(M, N, K, out=F32, c=True, beta=0.5, act=lg.GEMM_ACT_RELU).check("pipelined, C")
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_operand_past_4_gib(M):
+    """B of 4.6 GB: its columns past 2^32 bytes, and those next to where the call
+    takes the next part, in the result's first and last rows."""
+    N, K = 70000, 65536
+    g = torch.Generator(device="cuda").manual_seed(9)
+    A = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    B = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sB = torch.rand(N, device="cuda", generator=g) + 0.5
+    bias = torch.randn(N, device="cuda", generator=g)
+    D = torch.zeros(M, N, device="cuda")
+    st = lg.gemm_run_scaled(M, N, K, A.data_ptr(), K, R, B.data_ptr(), K, C, 0, sB.data_ptr(), 0, N,
+                            D.data_ptr(), N, lg.GEMM_I8, lg.GEMM_I32, F32, 0,
+                            lg.GemmEpilogue(bias=bias.data_ptr()), stream())
+    assert st == 0
+    cols = [0, 1, 65023, 65024, 65279, 65280, 65535, 65536, 69999]
+    want = A.double() @ B[cols].double().T
+    ref = (want * sB[cols].double() + bias[cols].double()).cpu()
+    assert ((D[:, cols].double().cpu() - ref).abs() <= 4 * 2.0 ** -24 * (ref.abs() + 8)).all()
+
+
 @pytest.mark.parametrize("la,lb", LAYOUTS)
 def test_medium_tiles(la, lb):
     Scaled(1500, 1600, 384, la, lb, out=BF16, bias=True).check("medium")
