@@ -181,22 +181,22 @@ __device__ inline void moe_weights(const MoeParams &p, int t, uint32_t *keys, fl
     }
 }
 
-// Slot blockIdx.y, columns of h in blocks of 16, one for each workgroup in
-// turn; the last workgroup of a slot (blockIdx.x == gridDim.x - 1) writes the
+// Slot blockIdx.y, columns of h in blocks of 16, one in turn for each workgroup
+// (KW = 4: its four waves split H) or for each wave (KW = 1: no exchange between
+// waves); the last workgroup of a slot (blockIdx.x == gridDim.x - 1) writes the
 // slot's tokens and the weights of token blockIdx.y, blockIdx.y + slots, ...
-// instead.  Four waves split H.  MT: row groups of 16 tokens in one pass over the
-// weights (1 for T <= 16, 2 otherwise), or 0 for T <= 4; an expert of few tokens
-// takes a shorter pass, one of more than 32 several.
+// instead.  MT = 1 takes the expert's tokens 16 at a time (or at most four, a
+// shorter pass), MT = 0 (T <= 4) four.
 constexpr int kMoeStaged = 4096;  // logits (or pairs) that are held in LDS
 
-template <int IT, bool W8, int MT, bool VEC>
+template <int IT, bool W8, int MT, int KW, bool VEC>
 __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
     __shared__ uint32_t keys[kMoeStaged];
     __shared__ float part[8];
     __shared__ int ranks[kMoeMaxTokens], list[kMoeMaxTokens], found[2];
-    constexpr int ROWS = MT == 0 ? 4 : 16 * MT;  // tokens of a pass
-    __shared__ f32x4 sums[4][MT == 2 ? 4 : 2][64];
+    constexpr int ROWS = MT == 0 ? 4 : 16;  // tokens of a pass
+    __shared__ f32x4 sums[KW][KW > 1 ? 2 : 1][KW > 1 ? 64 : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int slot = blockIdx.y, t0 = slot / p.topk, r0 = slot % p.topk;
     const bool own = p.slots != p.E;  // the slot is token t0's expert of rank r0
@@ -263,14 +263,33 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
     }
     if (n == 0) return;
 
-    const int groups = (p.H + S::KG - 1) / S::KG, per = (groups + 3) / 4;
-    const int gbeg = min(wave * per, groups), gend = min((wave + 1) * per, groups);
+    const int groups = (p.H + S::KG - 1) / S::KG, per = (groups + KW - 1) / KW;
+    const int kw = KW > 1 ? wave : 0;
+    const int gbeg = min(kw * per, groups), gend = min((kw + 1) * per, groups);
     const int64_t first = (int64_t)e * 2 * p.I;
     auto token = [&](int i) {  // rows past the last token repeat it; not stored
         return (uint32_t)(list[min(i, n - 1)] / p.topk) * (uint32_t)p.ldx * 2u;
     };
+    // h of row `row` of the list and columns c .. c + 3, from the gate's and up's sums
+    auto finish = [&](int row, int c, f32x4 g, f32x4 u) {
+        if (row >= n || c >= p.I) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (W8) {
+                const int cq = min(c + q, p.I - 1);
+                g[q] *= p.s1[first + cq];
+                u[q] *= p.s1[first + p.I + cq];
+            }
+            g[q] = moe_activate(g[q], p.act) * u[q];
+        }
+        // h is rounded to x's type: the second product's operand has to be of
+        // that type, and its rounding errors, of independent signs, come to about
+        // as much as y's own
+        moe_store4<IT>(p.h + (int64_t)list[row] * p.ldh * 2, c, p.I - c, true, g);
+    };
+    const int step = (4 / KW) * (gridDim.x - 1);
 #pragma nounroll
-    for (int jb = blockIdx.x; jb * 16 < p.I; jb += gridDim.x - 1) {
+    for (int jb = (4 / KW) * blockIdx.x + (KW > 1 ? 0 : wave); jb * 16 < p.I; jb += step) {
         const int lane = opaque(tid & 63);
         StreamRows w[2];
 #pragma unroll
@@ -280,71 +299,49 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
             });
 #pragma nounroll
         for (int n0 = 0; n0 < n; n0 += ROWS) {
-            int tiles = 1;
-            const int lane = opaque(tid & 63);
+            const int lane = opaque(tid & 63), r = lane & 15;
+            const int c = jb * 16 + 4 * (lane >> 4);
             bool few_rows = true;
             if constexpr (MT > 0) few_rows = n - n0 <= 4;
             if (few_rows) {
                 StreamFew<IT, W8, 2, VEC, VEC> few;
-                few.run(w, p.X, token(n0 + ((lane & 15) >> 2)), lane, gbeg, gend, p.H);
-                Unroll<0, 2>::run([&](auto ff) {
-                    constexpr int f = decltype(ff)::value;
-                    const f32x4 v = few.template sums<f>(lane);
-                    if ((lane & 3) == 0) sums[wave][f][(lane & 48) | ((lane & 15) >> 2)] = v;
-                });
-            } else if (MT > 0 && (MT == 1 || n - n0 <= 16)) {
+                few.run(w, p.X, token(n0 + (r >> 2)), lane, gbeg, gend, p.H);
+                const f32x4 g = few.template sums<0>(lane), u = few.template sums<1>(lane);
+                if constexpr (KW == 1) {
+                    if ((lane & 3) == 0) finish(n0 + (r >> 2), c, g, u);
+                } else if ((lane & 3) == 0) {
+                    sums[wave][0][(lane & 48) | (r >> 2)] = g;
+                    sums[wave][1][(lane & 48) | (r >> 2)] = u;
+                }
+            } else if constexpr (MT > 0) {
                 StreamRows x[1];
                 x[0].set(lane, p.X, [&](int i) { return token(n0 + i); });
                 f32x4 acc[1][2] = {};
                 Stream<IT, W8, 1, 2, false, VEC, VEC> stream;
                 stream.run(w, x, lane, gbeg, gend, p.H, acc);
-                sums[wave][0][lane] = acc[0][0];
-                sums[wave][1][lane] = acc[0][1];
-            } else if constexpr (MT == 2) {
-                tiles = 2;
-                StreamRows x[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    x[t].set(lane, p.X, [&](int i) { return token(n0 + 16 * t + i); });
-                f32x4 acc[2][2] = {};
-                Stream<IT, W8, 2, 2, false, VEC, VEC> stream;
-                stream.run(w, x, lane, gbeg, gend, p.H, acc);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) sums[wave][2 * t + f][lane] = acc[t][f];
-            }
-            __syncthreads();
-            // lane: row 16 t + lane % 16, four columns from 4 (lane / 16)
-            if (wave < tiles) {
-                const int t = wave, row = n0 + 16 * t + (lane & 15);
-                const int c = jb * 16 + 4 * (lane >> 4);
-                if (row < n && c < p.I) {
-                    f32x4 g = sums[0][2 * t][lane], u = sums[0][2 * t + 1][lane];
-#pragma unroll
-                    for (int z = 1; z < 4; ++z) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            g[q] += sums[z][2 * t][lane][q];
-                            u[q] += sums[z][2 * t + 1][lane][q];
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if constexpr (W8) {
-                            const int cq = min(c + q, p.I - 1);
-                            g[q] *= p.s1[first + cq];
-                            u[q] *= p.s1[first + p.I + cq];
-                        }
-                        g[q] = moe_activate(g[q], p.act) * u[q];
-                    }
-                    // h is rounded to x's type: the second product's operand has
-                    // to be of that type, and its rounding errors, of independent
-                    // signs, come to about as much as y's own
-                    moe_store4<IT>(p.h + (int64_t)list[row] * p.ldh * 2, c, p.I - c, true, g);
+                if constexpr (KW == 1) {
+                    finish(n0 + r, c, acc[0][0], acc[0][1]);
+                } else {
+                    sums[wave][0][lane] = acc[0][0];
+                    sums[wave][1][lane] = acc[0][1];
                 }
             }
-            __syncthreads();
+            if constexpr (KW > 1) {
+                __syncthreads();
+                if (wave == 0) {  // lane: row lane % 16, four columns from 4 (lane / 16)
+                    f32x4 g = sums[0][0][lane], u = sums[0][1][lane];
+#pragma unroll
+                    for (int z = 1; z < KW; ++z) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            g[q] += sums[z][0][lane][q];
+                            u[q] += sums[z][1][lane][q];
+                        }
+                    }
+                    finish(n0 + r, c, g, u);
+                }
+                __syncthreads();
+            }
         }
     }
 }
@@ -356,7 +353,7 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
 template <int IT, bool W8, int TM, int W, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
-    constexpr int MT = TM <= 4 ? 0 : (TM <= 16 ? 1 : 2), ROWS = MT == 0 ? 4 : 16 * MT;
+    constexpr int MT = TM <= 4 ? 0 : 1, ROWS = MT == 0 ? 4 : 16;
     __shared__ f32x4 y[W][TM][4];
     __shared__ int active[kMoeMaxExperts], count[kMoeMaxExperts], expert[kMoeMaxExperts], found;
     __shared__ int pairs[kMoeStaged];
@@ -428,29 +425,20 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
 #pragma nounroll
         for (int i0 = 0; i0 < n; i0 += ROWS) {
             const int lane = opaque(tid & 63), r = lane & 15;
-            if (MT == 0 || n - i0 <= 4) {
+            bool few_rows = true;
+            if constexpr (MT > 0) few_rows = n - i0 <= 4;
+            if (few_rows) {
                 StreamFew<IT, W8, 1, true, VEC> few;
                 few.run(w, p.h, hrow(i0 + (r >> 2)), lane, gbeg, gend, p.I);
                 const f32x4 v = few.template sums<0>(lane);
                 if ((lane & 3) == 0 && i0 + (r >> 2) < n) add(i0 + (r >> 2), v);
-            } else if (MT > 0 && (MT == 1 || n - i0 <= 16)) {
+            } else if constexpr (MT > 0) {
                 StreamRows x[1];
                 x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); });
                 f32x4 acc[1][1] = {};
                 Stream<IT, W8, 1, 1, false, true, VEC> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I, acc);
                 if (i0 + r < n) add(i0 + r, acc[0][0]);
-            } else if constexpr (MT == 2) {
-                StreamRows x[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    x[t].set(lane, p.h, [&](int i) { return hrow(i0 + 16 * t + i); });
-                f32x4 acc[2][1] = {};
-                Stream<IT, W8, 2, 1, false, true, VEC> stream;
-                stream.run(w, x, lane, gbeg, gend, p.I, acc);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (i0 + 16 * t + r < n) add(i0 + 16 * t + r, acc[t][0]);
             }
         }
     }
@@ -477,21 +465,28 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
 }
 
 template <int IT, bool W8, bool VEC>
-hipError_t moe_launch(const MoeParams &p, int up_blocks, hipStream_t s) {
+hipError_t moe_launch(const MoeParams &p, int cus, hipStream_t s) {
     MoeParams arg = p;
     void *args[] = {&arg};
-    const dim3 up((unsigned)up_blocks + 1, (unsigned)p.slots), down((unsigned)((p.H + 15) / 16));
+    // Blocks of 16 columns of every slot: one for each wave where that gives every
+    // CU eight waves, otherwise one for each workgroup.  Then about four workgroups
+    // for each CU; one takes several blocks where there are more.
+    const int64_t blocks = (p.I + 15) / 16;
+    const bool alone = blocks * p.slots >= 8 * (int64_t)cus;
+    const int64_t parts = alone ? (blocks + 3) / 4 : blocks;
+    const int64_t want = (4 * (int64_t)cus + p.slots - 1) / p.slots;
+    const dim3 up((unsigned)(parts < want ? parts : want) + 1, (unsigned)p.slots);
+    const dim3 down((unsigned)((p.H + 15) / 16));
     const void *k1, *k2;
-    if (p.T <= 4) {
-        k1 = (const void *)moe_up_kernel<IT, W8, 0, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 4, 8, VEC>;
-    } else if (p.T <= 16) {
-        k1 = (const void *)moe_up_kernel<IT, W8, 1, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 16, 8, VEC>;
-    } else {
-        k1 = (const void *)moe_up_kernel<IT, W8, 2, VEC>;
-        k2 = (const void *)moe_down_kernel<IT, W8, 64, 8, VEC>;
-    }
+    if (p.T <= 4)
+        k1 = alone ? (const void *)moe_up_kernel<IT, W8, 0, 1, VEC>
+                   : (const void *)moe_up_kernel<IT, W8, 0, 4, VEC>;
+    else
+        k1 = alone ? (const void *)moe_up_kernel<IT, W8, 1, 1, VEC>
+                   : (const void *)moe_up_kernel<IT, W8, 1, 4, VEC>;
+    k2 = p.T <= 4    ? (const void *)moe_down_kernel<IT, W8, 4, 8, VEC>
+         : p.T <= 16 ? (const void *)moe_down_kernel<IT, W8, 16, 8, VEC>
+                     : (const void *)moe_down_kernel<IT, W8, 64, 8, VEC>;
     const hipError_t st = hipLaunchKernel(k1, up, dim3(256), args, 0, s);
     if (st != hipSuccess) return st;
     return hipLaunchKernel(k2, down, dim3(512), args, 0, s);
@@ -499,9 +494,9 @@ hipError_t moe_launch(const MoeParams &p, int up_blocks, hipStream_t s) {
 
 // One translation unit for each type of x and w: moe_<x>.hip, moe_<x>_i8.hip.
 // vec: x and the weights allow 16-byte loads.
-hipError_t launch_moe_f16(const MoeParams &, int up_blocks, bool vec, hipStream_t);
-hipError_t launch_moe_bf16(const MoeParams &, int up_blocks, bool vec, hipStream_t);
-hipError_t launch_moe_f16_i8(const MoeParams &, int up_blocks, bool vec, hipStream_t);
-hipError_t launch_moe_bf16_i8(const MoeParams &, int up_blocks, bool vec, hipStream_t);
+hipError_t launch_moe_f16(const MoeParams &, int cus, bool vec, hipStream_t);
+hipError_t launch_moe_bf16(const MoeParams &, int cus, bool vec, hipStream_t);
+hipError_t launch_moe_f16_i8(const MoeParams &, int cus, bool vec, hipStream_t);
+hipError_t launch_moe_bf16_i8(const MoeParams &, int cus, bool vec, hipStream_t);
 
 }  // namespace libgemm

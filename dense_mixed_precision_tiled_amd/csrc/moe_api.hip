@@ -66,16 +66,13 @@ int gemm_moe_run(int64_t T, const gemm_moe_t *layer, const void *X, int64_t ldx,
     const bool vec = (uintptr_t)X % 16 == 0 && (uintptr_t)m.W1 % 16 == 0 &&
                      (uintptr_t)m.W2 % 16 == 0 && ldx % 8 == 0 && (m.ld1 * wsz) % 16 == 0 &&
                      (m.ld2 * wsz) % 16 == 0;
-    // about four workgroups of four waves for each CU; one takes several blocks
-    // of 16 columns where there are more
-    const int64_t blocks = cdiv(m.I, 16), want = cdiv(4 * (int64_t)topology().cus, w.slots);
-    const int up_blocks = (int)(blocks < want ? blocks : want);
+    const int cus = topology().cus;
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (in_dtype == GEMM_F16)
-        e = i8 ? launch_moe_f16_i8(p, up_blocks, vec, s) : launch_moe_f16(p, up_blocks, vec, s);
+        e = i8 ? launch_moe_f16_i8(p, cus, vec, s) : launch_moe_f16(p, cus, vec, s);
     else
-        e = i8 ? launch_moe_bf16_i8(p, up_blocks, vec, s) : launch_moe_bf16(p, up_blocks, vec, s);
+        e = i8 ? launch_moe_bf16_i8(p, cus, vec, s) : launch_moe_bf16(p, cus, vec, s);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 

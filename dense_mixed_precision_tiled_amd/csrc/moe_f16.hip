@@ -3,8 +3,8 @@
 #include "moe.hpp"
 
 namespace libgemm {
-hipError_t launch_moe_f16(const MoeParams &p, int up_blocks, bool vec, hipStream_t s) {
-    return vec ? moe_launch<IT_F16, false, true>(p, up_blocks, s)
-               : moe_launch<IT_F16, false, false>(p, up_blocks, s);
+hipError_t launch_moe_f16(const MoeParams &p, int cus, bool vec, hipStream_t s) {
+    return vec ? moe_launch<IT_F16, false, true>(p, cus, s)
+               : moe_launch<IT_F16, false, false>(p, cus, s);
 }
 }  // namespace libgemm
