@@ -299,37 +299,46 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
             });
 #pragma nounroll
         for (int n0 = 0; n0 < n; n0 += ROWS) {
-            const int lane = opaque(tid & 63), r = lane & 15;
+            const int lane = opaque(tid & 63);
             const int c = jb * 16 + 4 * (lane >> 4);
-            bool few_rows = true;
-            if constexpr (MT > 0) few_rows = n - n0 <= 4;
-            if (few_rows) {
-                StreamFew<IT, W8, 2, VEC, VEC> few;
-                few.run(w, p.X, token(n0 + (r >> 2)), lane, gbeg, gend, p.H);
-                const f32x4 g = few.template sums<0>(lane), u = few.template sums<1>(lane);
-                if constexpr (KW == 1) {
-                    if ((lane & 3) == 0) finish(n0 + (r >> 2), c, g, u);
-                } else if ((lane & 3) == 0) {
-                    sums[wave][0][(lane & 48) | (r >> 2)] = g;
-                    sums[wave][1][(lane & 48) | (r >> 2)] = u;
-                }
+            // sums of the gate and up products, and the lane's row of this pass
+            f32x4 g, u;
+            int row;
+            auto quads = [&](auto sets) {
+                constexpr int SETS = decltype(sets)::value;
+                StreamX<SETS> x;
+                x.set(lane, p.X, [&](int i) { return token(n0 + i); });
+                StreamQuads<IT, W8, SETS, 2, SETS == 1, VEC, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.H);
+                g = stream.template own_sums<0>(lane);
+                u = stream.template own_sums<1>(lane);
+                row = stream_row<SETS>(lane);
+            };
+            if (MT == 0 || n - n0 <= 4) {
+                quads(std::integral_constant<int, 1>{});
             } else if constexpr (MT > 0) {
-                StreamRows x[1];
-                x[0].set(lane, p.X, [&](int i) { return token(n0 + i); });
-                f32x4 acc[1][2] = {};
-                Stream<IT, W8, 1, 2, false, VEC, VEC> stream;
-                stream.run(w, x, lane, gbeg, gend, p.H, acc);
-                if constexpr (KW == 1) {
-                    finish(n0 + r, c, acc[0][0], acc[0][1]);
+                if (n - n0 <= 8) {
+                    quads(std::integral_constant<int, 2>{});
                 } else {
-                    sums[wave][0][lane] = acc[0][0];
-                    sums[wave][1][lane] = acc[0][1];
+                    StreamRows x[1];
+                    x[0].set(lane, p.X, [&](int i) { return token(n0 + i); });
+                    f32x4 acc[1][2] = {};
+                    StreamTiles<IT, W8, 1, 2, false, VEC, VEC> stream;
+                    stream.run(w, x, lane, gbeg, gend, p.H, acc);
+                    g = acc[0][0];
+                    u = acc[0][1];
+                    row = lane & 15;
                 }
+            }
+            if constexpr (KW == 1) {
+                finish(n0 + row, c, g, u);
+            } else {
+                sums[wave][0][lane] = g;
+                sums[wave][1][lane] = u;
             }
             if constexpr (KW > 1) {
                 __syncthreads();
-                if (wave == 0) {  // lane: row lane % 16, four columns from 4 (lane / 16)
-                    f32x4 g = sums[0][0][lane], u = sums[0][1][lane];
+                if (wave == 0) {
 #pragma unroll
                     for (int z = 1; z < KW; ++z) {
 #pragma unroll
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
                             u[q] += sums[z][1][lane][q];
                         }
                     }
-                    finish(n0 + r, c, g, u);
+                    finish(n0 + row, c, g, u);
                 }
                 __syncthreads();
             }
@@ -424,22 +433,34 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
         };
 #pragma nounroll
         for (int i0 = 0; i0 < n; i0 += ROWS) {
-            const int lane = opaque(tid & 63), r = lane & 15;
-            bool few_rows = true;
-            if constexpr (MT > 0) few_rows = n - i0 <= 4;
-            if (few_rows) {
-                StreamFew<IT, W8, 1, true, VEC> few;
-                few.run(w, p.h, hrow(i0 + (r >> 2)), lane, gbeg, gend, p.I);
-                const f32x4 v = few.template sums<0>(lane);
-                if ((lane & 3) == 0 && i0 + (r >> 2) < n) add(i0 + (r >> 2), v);
+            const int lane = opaque(tid & 63);
+            f32x4 v;
+            int row;
+            auto quads = [&](auto sets) {
+                constexpr int SETS = decltype(sets)::value;
+                StreamX<SETS> x;
+                x.set(lane, p.h, [&](int i) { return hrow(i0 + i); });
+                StreamQuads<IT, W8, SETS, 1, true, true, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.I);
+                v = stream.template own_sums<0>(lane);
+                row = stream_row<SETS>(lane);
+            };
+            if (MT == 0 || n - i0 <= 4) {
+                quads(std::integral_constant<int, 1>{});
             } else if constexpr (MT > 0) {
-                StreamRows x[1];
-                x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); });
-                f32x4 acc[1][1] = {};
-                Stream<IT, W8, 1, 1, false, true, VEC> stream;
-                stream.run(w, x, lane, gbeg, gend, p.I, acc);
-                if (i0 + r < n) add(i0 + r, acc[0][0]);
+                if (n - i0 <= 8) {
+                    quads(std::integral_constant<int, 2>{});
+                } else {
+                    StreamRows x[1];
+                    x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); });
+                    f32x4 acc[1][1] = {};
+                    StreamTiles<IT, W8, 1, 1, false, true, VEC> stream;
+                    stream.run(w, x, lane, gbeg, gend, p.I, acc);
+                    v = acc[0][0];
+                    row = lane & 15;
+                }
             }
+            if (i0 + row < n) add(i0 + row, v);
         }
     }
     __syncthreads();

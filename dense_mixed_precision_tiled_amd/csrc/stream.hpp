@@ -1,10 +1,10 @@
 // Products of a few rows with a weight matrix that is read once.
 //
-// y(r, j) = sum_k x(r, k) w(j, k) for up to 16 * MT rows of x: the arithmetic
-// for each byte of w is so little that the rate at which w arrives from memory
+// y(r, j) = sum_k x(r, k) w(j, k) for up to 32 rows of x: the arithmetic for
+// each byte of w is so little that the rate at which w arrives from memory
 // is all that counts.  So w goes from memory straight to the matrix units'
 // operand registers: a wave takes 16 rows of w (output channels) as the MFMA's
-// first operand and 16 rows of x as its second.  Staging w in LDS would add a
+// first operand and rows of x as its second.  Staging w in LDS would add a
 // write, a read and a wait to every byte without saving a load: no two waves
 // share a byte of w.  x is small and comes from the caches, once for every
 // 16 * NF channels.
@@ -12,15 +12,24 @@
 // The MFMA wants lane l to hold row l % 16, a part of k by l / 16.  Loaded in that
 // shape, neighbouring lanes are in different rows and every lane's 16 bytes are a
 // request of their own: 64 cycles of a CU's address path for each KiB, of w and of
-// x alike (16 x 16384 x 16384: 4.1 TB/s; 64 x 4096 x 16384: 1.7 TB/s).  So the four
-// lanes of a quad read 64 consecutive bytes of one row, four loads cover the
-// quad's four rows, and a 4 x 4 transpose inside the quad (DPP) gives each
-// lane 64 bytes of its own row.  The four quads with the same rows take
-// consecutive 64 bytes, so a load reads 256 consecutive bytes of four rows.
+// x alike (16 x 16384 x 16384 ran at 4.1 TB/s).  So the four lanes of a quad read
+// 64 consecutive bytes of one row, and the four quads with the same rows take
+// consecutive 64 bytes: a load reads 256 bytes of four rows, and four loads the
+// sixteen rows.
 //
-// Any order of k is right as long as x and w take the same one.  The waves of a
-// workgroup take consecutive parts of K and add their sums up in LDS, in a fixed
-// order: the same call gives the same bits.
+// The lanes of a quad then hold four different parts of k of one row of w.  With
+// x loaded alike (lane 4 t + d of a quad row: part d of row t), the MFMA forms,
+// for operand rows 4 j + c and columns 4 t + d, the product of part c of w with
+// part d of x: those with c == d are terms of the sums, the others are left
+// alone, and the sum over c is taken once, at the end (StreamQuads).  One MFMA
+// then serves four rows of x instead of sixteen, of which there is plenty for up
+// to eight rows.  For more, the parts are exchanged inside the quads (StreamTiles):
+// 64 vector instructions for every four loads, but sixteen rows for each MFMA and
+// accumulator (16 x 16384 x 4096: 15.0 us against 17.4; eight rows 15.0 against
+// 14.1).
+//
+// The waves of a workgroup that share a product take consecutive parts of K and
+// add their sums up in LDS, in a fixed order: the same call gives the same bits.
 #pragma once
 
 #include "gemm_kernels.hpp"
@@ -125,8 +134,8 @@ __device__ __forceinline__ uint32_t quad_xor(uint32_t v) {
 // Element m of lane c of every quad becomes element c of lane m: exchanges with
 // the neighbours at lane ^ 1 and lane ^ 2.  (64 vector instructions for four
 // 16-byte values.  One v_cndmask with its source read across the quad, written as
-// assembly, halves that, but ties the loads of a group together: 64 x 4096 x 16384
-// 33 us against 24.)
+// assembly, halves that, but ties the loads of a group together: 33 us against 24
+// at 64 x 4096 x 16384.)
 __device__ __forceinline__ void stream_transpose(u32x4 (&v)[4], int lane) {
     const bool b0 = lane & 1, b1 = lane & 2;
     auto swap1 = [&](uint32_t &lo, uint32_t &hi) {
@@ -150,24 +159,37 @@ __device__ __forceinline__ void stream_transpose(u32x4 (&v)[4], int lane) {
     });
 }
 
-// The 16 rows of one operand tile as a lane reads them: the byte offsets of the
-// four rows of its quad and of its own row from a common start.  The start is a
-// scalar that moves along K, so the loads need no vector arithmetic for their
-// addresses.
+// 16 rows of an operand as a lane reads them: the byte offsets of the four rows of its
+// quad from a common start.  The start is a scalar that moves along K, so the
+// loads need no vector arithmetic for their addresses.
 struct StreamRows {
     const uint8_t *base;
-    uint32_t o0, o1, o2, o3, own;
-    // row(i): byte offset of the tile's row i
+    uint32_t o0, o1, o2, o3;
+    // row(i): byte offset of row i
     template <class F>
     __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row) {
         const int i = lane & 12;
         base = start;
         o0 = row(i), o1 = row(i + 1), o2 = row(i + 2), o3 = row(i + 3);
-        own = row(lane & 15);
     }
     template <int M>
     __device__ __forceinline__ uint32_t quad() const {
         return M == 0 ? o0 : (M == 1 ? o1 : (M == 2 ? o2 : o3));
+    }
+};
+
+// Rows 4 s + (lane % 16) / 4 of x, s < SETS: byte offsets from a common start.
+template <int SETS>
+struct StreamX {
+    const uint8_t *base;
+    uint32_t o[SETS];
+    // row(i): byte offset of row i
+    template <class F>
+    __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row) {
+        base = start;
+        Unroll<0, SETS>::run([&](auto ss) {
+            o[decltype(ss)::value] = row(4 * decltype(ss)::value + ((lane & 15) >> 2));
+        });
     }
 };
 
@@ -176,11 +198,177 @@ __device__ __forceinline__ u32x4 stream_load(const uint8_t *base, uint32_t offse
     return *reinterpret_cast<const u32x4 *>(base + (uint64_t)offset);
 }
 
-// acc[t][f] += the products of groups [gbeg, gend) of K (KG values each) of the
-// weight rows w[f] and the rows x[t].  XV, WV: the rows allow 16-byte loads.  DB:
-// a group is in flight while the one before it is multiplied.
+// The sums over groups [gbeg, gend) of K (KG values each) of NF times 16 rows of w
+// and 4 SETS rows of x.  XV, WV: the rows allow 16-byte loads.  DB: a group is in
+// flight while the one before it is multiplied.
+template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV>
+struct StreamQuads {
+    using S = StreamTypes<XT, W8>;
+    static constexpr int XC = S::XC;
+    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][SETS][XC];
+    f32x4 acc[NF][4][SETS];  // [channel group][row of the quad][row set]
+
+    // a group that lies below K
+    template <int SL>
+    __device__ __forceinline__ void load(const StreamRows (&w)[NF], const StreamX<SETS> &x,
+                                         int lane, int g) {
+        const uint32_t o = (lane >> 4) * 64 + (lane & 3) * 16;
+        Unroll<0, 4>::run([&](auto mm) {
+            constexpr int m = decltype(mm)::value;
+            Unroll<0, NF>::run([&](auto ff) {
+                constexpr int f = decltype(ff)::value;
+                wv[SL][f][m] =
+                    stream_load(w[f].base + (int64_t)g * 256, w[f].template quad<m>() + o);
+            });
+        });
+        Unroll<0, SETS>::run([&](auto ss) {
+            Unroll<0, XC>::run([&](auto hh) {
+                constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
+                xv[SL][s][h] =
+                    stream_load(x.base + (int64_t)g * 256 * XC + 16 * h, x.o[s] + o * XC);
+            });
+        });
+    }
+    // any group, values at and past K zero
+    __device__ __forceinline__ void load_some(const StreamRows (&w)[NF], const StreamX<SETS> &x,
+                                              int lane, int g, int K) {
+        const int k = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * S::EPC;
+        Unroll<0, 4>::run([&](auto mm) {
+            constexpr int m = decltype(mm)::value;
+            Unroll<0, NF>::run([&](auto ff) {
+                constexpr int f = decltype(ff)::value;
+                wv[0][f][m] =
+                    stream_chunk<S::WES, WV>(w[f].base + w[f].template quad<m>(), k, K);
+            });
+        });
+        Unroll<0, SETS>::run([&](auto ss) {
+            Unroll<0, XC>::run([&](auto hh) {
+                constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
+                xv[0][s][h] =
+                    stream_chunk<S::XES, XV>(x.base + x.o[s], k + h * (16 / S::XES), K);
+            });
+        });
+    }
+    template <int SL>
+    __device__ __forceinline__ void multiply() {
+        Unroll<0, SETS>::run([&](auto ss) {
+            Unroll<0, XC>::run(
+                [&](auto hh) { arrive(xv[SL][decltype(ss)::value][decltype(hh)::value]); });
+        });
+        Unroll<0, NF>::run([&](auto ff) {
+            Unroll<0, 4>::run([&](auto mm) {
+                constexpr int f = decltype(ff)::value, m = decltype(mm)::value;
+                arrive(wv[SL][f][m]);
+                const u32x4 v = wv[SL][f][m];
+                if constexpr (W8) {
+                    const u32x4 a = stream_widen<XT>(v[0], v[1]), b = stream_widen<XT>(v[2], v[3]);
+                    Unroll<0, SETS>::run([&](auto ss) {
+                        constexpr int s = decltype(ss)::value;
+                        acc[f][m][s] = mfma16_1<XT>(a, xv[SL][s][0], acc[f][m][s]);
+                    });
+                    Unroll<0, SETS>::run([&](auto ss) {
+                        constexpr int s = decltype(ss)::value;
+                        acc[f][m][s] = mfma16_1<XT>(b, xv[SL][s][XC - 1], acc[f][m][s]);
+                    });
+                    // (chunk by chunk: all of a group's widened at once take 64 registers)
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    Unroll<0, SETS>::run([&](auto ss) {
+                        constexpr int s = decltype(ss)::value;
+                        acc[f][m][s] = mfma16_1<XT>(v, xv[SL][s][0], acc[f][m][s]);
+                    });
+                }
+            });
+        });
+    }
+    __device__ __forceinline__ void run(const StreamRows (&w)[NF], const StreamX<SETS> &x,
+                                        int lane, int gbeg, int gend, int K) {
+        Unroll<0, NF * 4 * SETS>::run([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            acc[i / SETS / 4][i / SETS % 4][i % SETS] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        });
+        int g = gbeg;
+        if constexpr (XV && WV) {
+            const int whole = min(gend, K / S::KG);  // groups that lie below K
+            if constexpr (DB) {
+                if (g < whole) load<0>(w, x, lane, g);
+#pragma nounroll
+                for (; g + 2 <= whole; g += 2) {
+                    load<1>(w, x, lane, g + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    multiply<0>();
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (g + 2 < whole) load<0>(w, x, lane, g + 2);
+                    __builtin_amdgcn_sched_barrier(0);
+                    multiply<DB ? 1 : 0>();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (g < whole) {
+                    multiply<0>();
+                    ++g;
+                }
+            } else {
+#pragma nounroll
+                for (; g < whole; ++g) {
+                    load<0>(w, x, lane, g);
+                    multiply<0>();
+                }
+            }
+        }
+#pragma nounroll
+        for (; g < gend; ++g) {
+            load_some(w, x, lane, g, K);
+            multiply<0>();
+        }
+    }
+    // The sums of channel group f and row set s: row 4 s + (lane % 16) / 4 of x,
+    // channels 4 (lane / 16) + 0 .. 3 (the lanes of a quad hold the same).
+    template <int f, int s>
+    __device__ __forceinline__ f32x4 sums(int lane) const {
+        f32x4 out;
+        Unroll<0, 4>::run([&](auto mm) {
+            constexpr int m = decltype(mm)::value;
+            const f32x4 a = acc[f][m][s];
+            const float v01 = lane & 1 ? a[1] : a[0], v23 = lane & 1 ? a[3] : a[2];
+            const uint32_t v = __float_as_uint(lane & 2 ? v23 : v01);
+            if constexpr (XT == IT_I8) {
+                const uint32_t p = v + quad_xor<1>(v);
+                out[m] = __uint_as_float(p + quad_xor<2>(p));
+            } else {
+                const float p = __uint_as_float(v) + __uint_as_float(quad_xor<1>(v));
+                out[m] = p + __uint_as_float(quad_xor<2>(__float_as_uint(p)));
+            }
+        });
+        return out;
+    }
+    // The sums of channel group f and row stream_row<SETS>(lane) + 16 R: up to four
+    // row sets at once, lane d of a quad taking set 4 R + d.
+    template <int f, int R = 0>
+    __device__ __forceinline__ f32x4 own_sums(int lane) const {
+        f32x4 out = sums<f, 4 * R>(lane);
+        Unroll<1, (SETS - 4 * R < 4 ? SETS - 4 * R : 4)>::run([&](auto dd) {
+            constexpr int d = decltype(dd)::value;
+            const f32x4 v = sums<f, 4 * R + d>(lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = (lane & 3) == d ? v[e] : out[e];
+        });
+        return out;
+    }
+};
+
+// The row whose sums own_sums gives a lane: 4 d + (lane % 16) / 4 for lane d of its
+// quad, or none (a row past every count) where d is not below SETS.
+template <int SETS>
+__device__ __forceinline__ int stream_row(int lane) {
+    const int d = lane & 3;
+    return d < SETS ? 4 * d + ((lane & 15) >> 2) : 1 << 20;
+}
+
+// The same for MT times 16 rows of x, exchanged inside the quads (x and w alike) so
+// that one MFMA serves 16 rows: acc[t][f] += the products of w[f] and x[t].  Lane l
+// of acc holds row l % 16 of x, channels 4 (l / 16) + 0 .. 3.
 template <int XT, bool W8, int MT, int NF, bool DB, bool XV, bool WV>
-struct Stream {
+struct StreamTiles {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
     u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][MT][XC][4];
@@ -207,32 +395,35 @@ struct Stream {
             });
         });
     }
-    // chunk w of channel group f with the one or two chunks of x that go with it
-    template <int f>
-    __device__ __forceinline__ static void mac(const u32x4 &w, const u32x4 (&x)[MT][XC],
-                                               f32x4 (&acc)[MT][NF]) {
-        if constexpr (W8) {
-            const u32x4 a = stream_widen<XT>(w[0], w[1]), b = stream_widen<XT>(w[2], w[3]);
+    // any group, values at and past K zero
+    __device__ __forceinline__ void load_some(const StreamRows (&w)[NF], const StreamRows (&x)[MT],
+                                              int lane, int g, int K) {
+        const int kw = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * S::EPC;
+        const int kx = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * (16 / S::XES);
+        Unroll<0, 4>::run([&](auto mm) {
+            constexpr int m = decltype(mm)::value;
+            Unroll<0, NF>::run([&](auto ff) {
+                constexpr int f = decltype(ff)::value;
+                wv[0][f][m] =
+                    stream_chunk<S::WES, WV>(w[f].base + w[f].template quad<m>(), kw, K);
+            });
+        });
+        Unroll<0, 4 * XC>::run([&](auto mm) {
+            constexpr int h = decltype(mm)::value / 4, m = decltype(mm)::value % 4;
             Unroll<0, MT>::run([&](auto tt) {
                 constexpr int t = decltype(tt)::value;
-                acc[t][f] = mfma16_1<XT>(a, x[t][0], acc[t][f]);
-                acc[t][f] = mfma16_1<XT>(b, x[t][XC - 1], acc[t][f]);
+                xv[0][t][h][m] = stream_chunk<S::XES, XV>(x[t].base + x[t].template quad<m>(),
+                                                          kx + 64 / S::XES * h, K);
             });
-        } else {
-            Unroll<0, MT>::run([&](auto tt) {
-                constexpr int t = decltype(tt)::value;
-                acc[t][f] = mfma16_1<XT>(w, x[t][0], acc[t][f]);
-            });
-        }
+        });
     }
     template <int SL>
     __device__ __forceinline__ void multiply(f32x4 (&acc)[MT][NF], int lane) {
         Unroll<0, MT>::run([&](auto tt) {
             Unroll<0, XC>::run([&](auto hh) {
-                Unroll<0, 4>::run([&](auto mm) {
-                    arrive(xv[SL][decltype(tt)::value][decltype(hh)::value][decltype(mm)::value]);
-                });
-                stream_transpose(xv[SL][decltype(tt)::value][decltype(hh)::value], lane);
+                constexpr int t = decltype(tt)::value, h = decltype(hh)::value;
+                Unroll<0, 4>::run([&](auto mm) { arrive(xv[SL][t][h][decltype(mm)::value]); });
+                stream_transpose(xv[SL][t][h], lane);
             });
         });
         Unroll<0, NF>::run([&](auto ff) {
@@ -240,18 +431,24 @@ struct Stream {
             Unroll<0, 4>::run([&](auto mm) { arrive(wv[SL][f][decltype(mm)::value]); });
             stream_transpose(wv[SL][f], lane);
             Unroll<0, 4>::run([&](auto mm) {
-                // the lane's chunk m of w: x's chunk m, or with two chunks of x for
-                // each of w's its chunks 2m and 2m + 1 of 128 bytes
+                // the lane's chunk m of w goes with x's chunk m, or with two chunks of
+                // x for each of w's with its chunks 2 m and 2 m + 1 of 128 bytes
                 constexpr int m = decltype(mm)::value;
-                u32x4 xm[MT][XC];
-                Unroll<0, MT>::run([&](auto tt) {
-                    constexpr int t = decltype(tt)::value;
-                    Unroll<0, XC>::run([&](auto hh) {
-                        constexpr int c = m * XC + decltype(hh)::value;
-                        xm[t][decltype(hh)::value] = xv[SL][t][c / 4][c % 4];
+                const u32x4 v = wv[SL][f][m];
+                if constexpr (W8) {
+                    const u32x4 a = stream_widen<XT>(v[0], v[1]), b = stream_widen<XT>(v[2], v[3]);
+                    Unroll<0, MT>::run([&](auto tt) {
+                        constexpr int t = decltype(tt)::value, c = 2 * m;
+                        acc[t][f] = mfma16_1<XT>(a, xv[SL][t][c / 4 % XC][c % 4], acc[t][f]);
+                        acc[t][f] = mfma16_1<XT>(b, xv[SL][t][c / 4 % XC][c % 4 + 1], acc[t][f]);
                     });
-                });
-                mac<f>(wv[SL][f][m], xm, acc);
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    Unroll<0, MT>::run([&](auto tt) {
+                        constexpr int t = decltype(tt)::value;
+                        acc[t][f] = mfma16_1<XT>(v, xv[SL][t][0][m], acc[t][f]);
+                    });
+                }
             });
         });
     }
@@ -286,147 +483,11 @@ struct Stream {
                 }
             }
         }
-        // what is left: blocks of 64 bytes of a row, in the MFMA's own shape,
-        // values at and past K zero
-        if (g >= gend) return;
-        const uint8_t *wr[NF], *xr[MT];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) wr[f] = w[f].base + w[f].own;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) xr[t] = x[t].base + x[t].own;
-        const int bend = min(4 * gend, (K + S::KB - 1) / S::KB);
 #pragma nounroll
-        for (int b = 4 * g; b < bend; ++b) {
-            const int k = b * S::KB + (lane >> 4) * S::EPC;
-            u32x4 xm[MT][XC];
-            Unroll<0, MT>::run([&](auto tt) {
-                constexpr int t = decltype(tt)::value;
-                Unroll<0, XC>::run([&](auto hh) {
-                    constexpr int h = decltype(hh)::value;
-                    xm[t][h] = stream_chunk<S::XES, XV>(xr[t], k + h * (16 / S::XES), K);
-                });
-            });
-            Unroll<0, NF>::run([&](auto ff) {
-                constexpr int f = decltype(ff)::value;
-                mac<f>(stream_chunk<S::WES, WV>(wr[f], k, K), xm, acc);
-            });
+        for (; g < gend; ++g) {
+            load_some(w, x, lane, g, K);
+            multiply<0>(acc, lane);
         }
-    }
-};
-
-// The same for at most four rows of x, without the transposes.  A quad's lanes
-// hold four different parts of k of one row of w, so the MFMA forms, for operand
-// rows 4 j + c and columns 4 t + d, the product of part c of w with part d of x:
-// those with c == d are terms of the sum, the others are left alone.  The sum
-// over c is taken once, at the end.  One MFMA then serves four rows of x instead
-// of sixteen, which costs nothing here, and x takes one load for every four of w.
-template <int XT, bool W8, int NF, bool XV, bool WV>
-struct StreamFew {
-    using S = StreamTypes<XT, W8>;
-    static constexpr int XC = S::XC;
-    u32x4 wv[2][NF][4], xv[2][XC];
-    f32x4 acc[NF][4], rest[NF];
-
-    template <int SL>
-    __device__ __forceinline__ void load(const StreamRows (&w)[NF], const uint8_t *x,
-                                         uint32_t xrow, int lane, int g) {
-        const uint32_t o = (lane >> 4) * 64 + (lane & 3) * 16;
-        Unroll<0, 4>::run([&](auto mm) {
-            constexpr int m = decltype(mm)::value;
-            Unroll<0, NF>::run([&](auto ff) {
-                constexpr int f = decltype(ff)::value;
-                wv[SL][f][m] =
-                    stream_load(w[f].base + (int64_t)g * 256, w[f].template quad<m>() + o);
-            });
-        });
-        Unroll<0, XC>::run([&](auto hh) {
-            constexpr int h = decltype(hh)::value;
-            xv[SL][h] = stream_load(x + (int64_t)g * 256 * XC + 16 * h, xrow + o * XC);
-        });
-    }
-    __device__ __forceinline__ static f32x4 mac(const u32x4 &w, const u32x4 (&x)[XC], f32x4 a) {
-        if constexpr (W8) {
-            a = mfma16_1<XT>(stream_widen<XT>(w[0], w[1]), x[0], a);
-            return mfma16_1<XT>(stream_widen<XT>(w[2], w[3]), x[XC - 1], a);
-        } else {
-            return mfma16_1<XT>(w, x[0], a);
-        }
-    }
-    template <int SL>
-    __device__ __forceinline__ void multiply() {
-        Unroll<0, XC>::run([&](auto hh) { arrive(xv[SL][decltype(hh)::value]); });
-        Unroll<0, NF>::run([&](auto ff) {
-            Unroll<0, 4>::run([&](auto mm) {
-                constexpr int f = decltype(ff)::value, m = decltype(mm)::value;
-                arrive(wv[SL][f][m]);
-                acc[f][m] = mac(wv[SL][f][m], xv[SL], acc[f][m]);
-            });
-        });
-    }
-    // x + xrow: start of row (lane % 16) / 4 of x
-    __device__ __forceinline__ void run(const StreamRows (&w)[NF], const uint8_t *x, uint32_t xrow,
-                                        int lane, int gbeg, int gend, int K) {
-        Unroll<0, NF>::run([&](auto ff) {
-            constexpr int f = decltype(ff)::value;
-            rest[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            Unroll<0, 4>::run([&](auto mm) { acc[f][decltype(mm)::value] = rest[f]; });
-        });
-        int g = gbeg;
-        if constexpr (XV && WV) {
-            const int whole = min(gend, K / S::KG);
-            if (g < whole) load<0>(w, x, xrow, lane, g);
-#pragma nounroll
-            for (; g + 2 <= whole; g += 2) {
-                load<1>(w, x, xrow, lane, g + 1);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply<0>();
-                __builtin_amdgcn_sched_barrier(0);
-                if (g + 2 < whole) load<0>(w, x, xrow, lane, g + 2);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply<1>();
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (g < whole) {
-                multiply<0>();
-                ++g;
-            }
-        }
-        if (g >= gend) return;
-        // what is left in the MFMA's own shape: the four columns of a quad are alike
-        const int bend = min(4 * gend, (K + S::KB - 1) / S::KB);
-#pragma nounroll
-        for (int b = 4 * g; b < bend; ++b) {
-            const int k = b * S::KB + (lane >> 4) * S::EPC;
-            u32x4 xm[XC];
-            Unroll<0, XC>::run([&](auto hh) {
-                constexpr int h = decltype(hh)::value;
-                xm[h] = stream_chunk<S::XES, XV>(x + xrow, k + h * (16 / S::XES), K);
-            });
-            Unroll<0, NF>::run([&](auto ff) {
-                constexpr int f = decltype(ff)::value;
-                rest[f] = mac(stream_chunk<S::WES, WV>(w[f].base + w[f].own, k, K), xm, rest[f]);
-            });
-        }
-    }
-    // The sums of channel group f: row (lane % 16) / 4 of x, channels
-    // 4 (lane / 16) + 0 .. 3 (the lanes of a quad hold the same).
-    template <int f>
-    __device__ __forceinline__ f32x4 sums(int lane) const {
-        f32x4 out;
-        Unroll<0, 4>::run([&](auto mm) {
-            constexpr int m = decltype(mm)::value;
-            const f32x4 a = acc[f][m];
-            const float v01 = lane & 1 ? a[1] : a[0], v23 = lane & 1 ? a[3] : a[2];
-            const uint32_t v = __float_as_uint(lane & 2 ? v23 : v01);
-            if constexpr (XT == IT_I8) {
-                const uint32_t p = v + quad_xor<1>(v);
-                out[m] = __uint_as_float(p + quad_xor<2>(p) + __float_as_uint(rest[f][m]));
-            } else {
-                const float p = __uint_as_float(v) + __uint_as_float(quad_xor<1>(v));
-                out[m] = p + __uint_as_float(quad_xor<2>(__float_as_uint(p))) + rest[f][m];
-            }
-        });
-        return out;
     }
 };
 
