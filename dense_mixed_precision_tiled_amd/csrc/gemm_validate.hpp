@@ -181,7 +181,7 @@ inline MoeWorkspace moe_workspace(int64_t T, const gemm_moe_t *m) {
     w.pairs = w.expert + 4 * w.slots;
     w.weight = w.pairs + 4 * w.slots * T;
     w.h = (w.weight + 4 * npairs + 255) / 256 * 256;
-    w.bytes = w.h + 2 * npairs * w.ldh + 255;
+    w.bytes = w.h + 2 * 2 * npairs * w.ldh + 255;  // two parts of 16-bit values
     return w;
 }
 

@@ -40,8 +40,9 @@ struct MoeParams {
     int *expert;    // [slots]
     int *pairs;     // [slots][T] token * topk + rank, ascending
     float *weight;  // [T * topk] weight of each pair
-    uint8_t *h;     // [T * topk][ldh] in the type of x
+    uint8_t *h;     // [2][T * topk][ldh] in the type of x: the values, and what is left of them
     int ldh;
+    __host__ __device__ int64_t h_low() const { return (int64_t)T * topk * ldh * 2; }
 };
 
 enum { MOE_SILU = 3 };  // beside ACT_*
@@ -115,6 +116,13 @@ template <int IT>
 __device__ __forceinline__ uint16_t moe_round(float v) {
     constexpr int OUT = IT == IT_F16 ? DT_F16 : DT_BF16;
     return (uint16_t)to_out16<OUT>(v, false);
+}
+
+// What rounding v leaves of it; 0 where the rounded value is not finite.
+template <int IT>
+__device__ __forceinline__ float moe_rest(float v) {
+    const float r = from_out16<IT == IT_F16 ? DT_F16 : DT_BF16>(moe_round<IT>(v));
+    return fabsf(r) < __builtin_inff() ? v - r : 0.0f;
 }
 
 // Four values of 16 bits, as many of them as n.
@@ -282,10 +290,17 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
             }
             g[q] = moe_activate(g[q], p.act) * u[q];
         }
-        // h is rounded to x's type: the second product's operand has to be of
-        // that type, and its rounding errors, of independent signs, come to about
-        // as much as y's own
-        moe_store4<IT>(p.h + (int64_t)list[row] * p.ldh * 2, c, p.I - c, true, g);
+        // h as the sum of two values of x's type, which the second product's operand
+        // has to be of.  Rounded to one value, its errors come to as much as y's own
+        // rounding (1.41 times that together: 0.0024 against 0.0017 of y's norm for
+        // bf16); 16 bits of h, or 22, leave them out.  It costs the second kernel the
+        // reads of h twice: 48 -> 53 us for 16 tokens and experts of 2048 x 1024,
+        // 57 -> 71 for 64 tokens and int8 experts of 4096 x 2048.
+        uint8_t *const to = p.h + (int64_t)list[row] * p.ldh * 2;
+        moe_store4<IT>(to, c, p.I - c, true, g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[q] = moe_rest<IT>(g[q]);
+        moe_store4<IT>(to + p.h_low(), c, p.I - c, true, g);
     };
     const int step = (4 / KW) * (gridDim.x - 1);
 #pragma nounroll
@@ -308,7 +323,9 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
                 constexpr int SETS = decltype(sets)::value;
                 StreamX<SETS> x;
                 x.set(lane, p.X, [&](int i) { return token(n0 + i); });
-                StreamQuads<IT, W8, SETS, 2, SETS == 1, VEC, VEC> stream;
+                // (a second group in flight takes registers that MT = 0 has better use
+                // for: 27.3 -> 26.9 us for a layer of one token; 149 -> 142 us at 16)
+                StreamQuads<IT, W8, SETS, 2, (MT > 0 && SETS == 1), VEC, VEC> stream;
                 stream.run(w, x, lane, gbeg, gend, p.H);
                 g = stream.template own_sums<0>(lane);
                 u = stream.template own_sums<1>(lane);
@@ -358,7 +375,9 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
 // Workgroup b computes columns [16 b, 16 b + 16) of y.  W waves share the
 // (expert, part of I) units; each adds w * (h D_e^T) to its own copy of y in LDS
 // (16 columns of every token), and the copies are added in order.  TM: the most
-// tokens.
+// tokens.  Passes of at most two tokens hold both parts of h in one set of rows,
+// longer ones take a second operand for each of w's; those of up to 12 tokens need
+// no exchanges (10.3 us for one token and 8 experts of 2048 x 1024: 3.3 TB/s).
 template <int IT, bool W8, int TM, int W, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
@@ -439,22 +458,38 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
             auto quads = [&](auto sets) {
                 constexpr int SETS = decltype(sets)::value;
                 StreamX<SETS> x;
-                x.set(lane, p.h, [&](int i) { return hrow(i0 + i); });
-                StreamQuads<IT, W8, SETS, 1, true, true, VEC> stream;
+                x.set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
+                StreamQuads<IT, W8, SETS, 1, SETS == 1, true, VEC, 2> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I);
                 v = stream.template own_sums<0>(lane);
                 row = stream_row<SETS>(lane);
             };
-            if (MT == 0 || n - i0 <= 4) {
+            if (n - i0 <= 2) {
+                // both parts of h in one set: rows 0 and 1 the values, 2 and 3 the rests
+                StreamX<1> x;
+                x.set(lane, p.h, [&](int i) {
+                    return hrow(i0 + (i & 1)) + (i & 2 ? (uint32_t)p.h_low() : 0u);
+                });
+                StreamQuads<IT, W8, 1, 1, true, true, VEC> stream;
+                stream.run(w, x, lane, gbeg, gend, p.I);
+                v = stream.template own_sums<0>(lane);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)  // row_ror 8: lane l's neighbour at l ^ 8
+                    v[q] += __int_as_float(
+                        __builtin_amdgcn_mov_dpp(__float_as_int(v[q]), 0x128, 0xf, 0xf, true));
+                row = stream_row<1>(lane);
+            } else if (MT == 0 || n - i0 <= 4) {
                 quads(std::integral_constant<int, 1>{});
             } else if constexpr (MT > 0) {
                 if (n - i0 <= 8) {
                     quads(std::integral_constant<int, 2>{});
+                } else if (n - i0 <= 12) {
+                    quads(std::integral_constant<int, 3>{});
                 } else {
                     StreamRows x[1];
-                    x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); });
+                    x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
                     f32x4 acc[1][1] = {};
-                    StreamTiles<IT, W8, 1, 1, false, true, VEC> stream;
+                    StreamTiles<IT, W8, 1, 1, false, true, VEC, 2> stream;
                     stream.run(w, x, lane, gbeg, gend, p.I, acc);
                     v = acc[0][0];
                     row = lane & 15;

@@ -164,12 +164,15 @@ __device__ __forceinline__ void stream_transpose(u32x4 (&v)[4], int lane) {
 // loads need no vector arithmetic for their addresses.
 struct StreamRows {
     const uint8_t *base;
+    int64_t low;  // of x in two parts: bytes from the first one to the second
     uint32_t o0, o1, o2, o3;
     // row(i): byte offset of row i
     template <class F>
-    __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row) {
+    __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row,
+                                        int64_t second = 0) {
         const int i = lane & 12;
         base = start;
+        low = second;
         o0 = row(i), o1 = row(i + 1), o2 = row(i + 2), o3 = row(i + 3);
     }
     template <int M>
@@ -182,11 +185,14 @@ struct StreamRows {
 template <int SETS>
 struct StreamX {
     const uint8_t *base;
+    int64_t low;  // x in two parts: bytes from the first one to the second
     uint32_t o[SETS];
     // row(i): byte offset of row i
     template <class F>
-    __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row) {
+    __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row,
+                                        int64_t second = 0) {
         base = start;
+        low = second;
         Unroll<0, SETS>::run([&](auto ss) {
             o[decltype(ss)::value] = row(4 * decltype(ss)::value + ((lane & 15) >> 2));
         });
@@ -200,12 +206,13 @@ __device__ __forceinline__ u32x4 stream_load(const uint8_t *base, uint32_t offse
 
 // The sums over groups [gbeg, gend) of K (KG values each) of NF times 16 rows of w
 // and 4 SETS rows of x.  XV, WV: the rows allow 16-byte loads.  DB: a group is in
-// flight while the one before it is multiplied.
-template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV>
+// flight while the one before it is multiplied.  XP = 2: x is the sum of two matrices
+// of its type (a value and what its rounding left).
+template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV, int XP = 1>
 struct StreamQuads {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
-    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][SETS][XC];
+    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][SETS][XP * XC];
     f32x4 acc[NF][4][SETS];  // [channel group][row of the quad][row set]
 
     // a group that lies below K
@@ -222,10 +229,11 @@ struct StreamQuads {
             });
         });
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XC>::run([&](auto hh) {
+            Unroll<0, XP * XC>::run([&](auto hh) {
                 constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
+                const uint8_t *from = h < XC ? x.base : x.base + x.low;
                 xv[SL][s][h] =
-                    stream_load(x.base + (int64_t)g * 256 * XC + 16 * h, x.o[s] + o * XC);
+                    stream_load(from + (int64_t)g * 256 * XC + 16 * (h % XC), x.o[s] + o * XC);
             });
         });
     }
@@ -242,17 +250,18 @@ struct StreamQuads {
             });
         });
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XC>::run([&](auto hh) {
+            Unroll<0, XP * XC>::run([&](auto hh) {
                 constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
+                const uint8_t *from = h < XC ? x.base : x.base + x.low;
                 xv[0][s][h] =
-                    stream_chunk<S::XES, XV>(x.base + x.o[s], k + h * (16 / S::XES), K);
+                    stream_chunk<S::XES, XV>(from + x.o[s], k + h % XC * (16 / S::XES), K);
             });
         });
     }
     template <int SL>
     __device__ __forceinline__ void multiply() {
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XC>::run(
+            Unroll<0, XP * XC>::run(
                 [&](auto hh) { arrive(xv[SL][decltype(ss)::value][decltype(hh)::value]); });
         });
         Unroll<0, NF>::run([&](auto ff) {
@@ -262,20 +271,17 @@ struct StreamQuads {
                 const u32x4 v = wv[SL][f][m];
                 if constexpr (W8) {
                     const u32x4 a = stream_widen<XT>(v[0], v[1]), b = stream_widen<XT>(v[2], v[3]);
-                    Unroll<0, SETS>::run([&](auto ss) {
-                        constexpr int s = decltype(ss)::value;
-                        acc[f][m][s] = mfma16_1<XT>(a, xv[SL][s][0], acc[f][m][s]);
-                    });
-                    Unroll<0, SETS>::run([&](auto ss) {
-                        constexpr int s = decltype(ss)::value;
-                        acc[f][m][s] = mfma16_1<XT>(b, xv[SL][s][XC - 1], acc[f][m][s]);
+                    Unroll<0, XP * XC * SETS>::run([&](auto ss) {
+                        constexpr int s = decltype(ss)::value % SETS, h = decltype(ss)::value / SETS;
+                        acc[f][m][s] =
+                            mfma16_1<XT>(h % XC == 0 ? a : b, xv[SL][s][h], acc[f][m][s]);
                     });
                     // (chunk by chunk: all of a group's widened at once take 64 registers)
                     __builtin_amdgcn_sched_barrier(0);
                 } else {
-                    Unroll<0, SETS>::run([&](auto ss) {
-                        constexpr int s = decltype(ss)::value;
-                        acc[f][m][s] = mfma16_1<XT>(v, xv[SL][s][0], acc[f][m][s]);
+                    Unroll<0, XP * SETS>::run([&](auto ss) {
+                        constexpr int s = decltype(ss)::value % SETS, h = decltype(ss)::value / SETS;
+                        acc[f][m][s] = mfma16_1<XT>(v, xv[SL][s][h], acc[f][m][s]);
                     });
                 }
             });
@@ -367,11 +373,11 @@ __device__ __forceinline__ int stream_row(int lane) {
 // The same for MT times 16 rows of x, exchanged inside the quads (x and w alike) so
 // that one MFMA serves 16 rows: acc[t][f] += the products of w[f] and x[t].  Lane l
 // of acc holds row l % 16 of x, channels 4 (l / 16) + 0 .. 3.
-template <int XT, bool W8, int MT, int NF, bool DB, bool XV, bool WV>
+template <int XT, bool W8, int MT, int NF, bool DB, bool XV, bool WV, int XP = 1>
 struct StreamTiles {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
-    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][MT][XC][4];
+    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][MT][XP * XC][4];
 
     template <int SL>
     __device__ __forceinline__ void load(const StreamRows (&w)[NF], const StreamRows (&x)[MT],
@@ -386,11 +392,12 @@ struct StreamTiles {
                     stream_load(w[f].base + (int64_t)g * 256, w[f].template quad<m>() + wo);
             });
         });
-        Unroll<0, 4 * XC>::run([&](auto mm) {
+        Unroll<0, 4 * XP * XC>::run([&](auto mm) {
             constexpr int h = decltype(mm)::value / 4, m = decltype(mm)::value % 4;
             Unroll<0, MT>::run([&](auto tt) {
                 constexpr int t = decltype(tt)::value;
-                xv[SL][t][h][m] = stream_load(x[t].base + (int64_t)g * 256 * XC + 64 * h,
+                const uint8_t *from = h < XC ? x[t].base : x[t].base + x[t].low;
+                xv[SL][t][h][m] = stream_load(from + (int64_t)g * 256 * XC + 64 * (h % XC),
                                               x[t].template quad<m>() + xo);
             });
         });
@@ -408,19 +415,20 @@ struct StreamTiles {
                     stream_chunk<S::WES, WV>(w[f].base + w[f].template quad<m>(), kw, K);
             });
         });
-        Unroll<0, 4 * XC>::run([&](auto mm) {
+        Unroll<0, 4 * XP * XC>::run([&](auto mm) {
             constexpr int h = decltype(mm)::value / 4, m = decltype(mm)::value % 4;
             Unroll<0, MT>::run([&](auto tt) {
                 constexpr int t = decltype(tt)::value;
-                xv[0][t][h][m] = stream_chunk<S::XES, XV>(x[t].base + x[t].template quad<m>(),
-                                                          kx + 64 / S::XES * h, K);
+                const uint8_t *from = h < XC ? x[t].base : x[t].base + x[t].low;
+                xv[0][t][h][m] = stream_chunk<S::XES, XV>(from + x[t].template quad<m>(),
+                                                          kx + 64 / S::XES * (h % XC), K);
             });
         });
     }
     template <int SL>
     __device__ __forceinline__ void multiply(f32x4 (&acc)[MT][NF], int lane) {
         Unroll<0, MT>::run([&](auto tt) {
-            Unroll<0, XC>::run([&](auto hh) {
+            Unroll<0, XP * XC>::run([&](auto hh) {
                 constexpr int t = decltype(tt)::value, h = decltype(hh)::value;
                 Unroll<0, 4>::run([&](auto mm) { arrive(xv[SL][t][h][decltype(mm)::value]); });
                 stream_transpose(xv[SL][t][h], lane);
@@ -437,16 +445,17 @@ struct StreamTiles {
                 const u32x4 v = wv[SL][f][m];
                 if constexpr (W8) {
                     const u32x4 a = stream_widen<XT>(v[0], v[1]), b = stream_widen<XT>(v[2], v[3]);
-                    Unroll<0, MT>::run([&](auto tt) {
-                        constexpr int t = decltype(tt)::value, c = 2 * m;
-                        acc[t][f] = mfma16_1<XT>(a, xv[SL][t][c / 4 % XC][c % 4], acc[t][f]);
-                        acc[t][f] = mfma16_1<XT>(b, xv[SL][t][c / 4 % XC][c % 4 + 1], acc[t][f]);
+                    Unroll<0, MT * XP>::run([&](auto tt) {
+                        constexpr int t = decltype(tt)::value % MT, c = 2 * m;
+                        constexpr int h = decltype(tt)::value / MT * XC + c / 4 % XC;
+                        acc[t][f] = mfma16_1<XT>(a, xv[SL][t][h][c % 4], acc[t][f]);
+                        acc[t][f] = mfma16_1<XT>(b, xv[SL][t][h][c % 4 + 1], acc[t][f]);
                     });
                     __builtin_amdgcn_sched_barrier(0);
                 } else {
-                    Unroll<0, MT>::run([&](auto tt) {
-                        constexpr int t = decltype(tt)::value;
-                        acc[t][f] = mfma16_1<XT>(v, xv[SL][t][0][m], acc[t][f]);
+                    Unroll<0, MT * XP>::run([&](auto tt) {
+                        constexpr int t = decltype(tt)::value % MT, h = decltype(tt)::value / MT;
+                        acc[t][f] = mfma16_1<XT>(v, xv[SL][t][h][m], acc[t][f]);
                     });
                 }
             });

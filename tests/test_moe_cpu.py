@@ -59,8 +59,8 @@ def test_workspace(T, E, topk, I):
     m = layer(E=E, topk=topk, I=I)
     n = lg.gemm_moe_workspace(T, m)
     pairs = T * topk
-    # the pairs' inner rows, and less than 16 bytes for each slot and token beside them
-    assert 2 * pairs * I <= n <= 2 * pairs * (I + 7) + 4 * (2 + T) * min(E, pairs) + 4 * pairs + 600
+    # the pairs' inner rows (two values of 16 bits each), and less than 16 bytes for each slot and token beside them
+    assert 4 * pairs * I <= n <= 4 * pairs * (I + 7) + 4 * (2 + T) * min(E, pairs) + 4 * pairs + 600
     args = dict(T=T, m=m, ldl=E)
     assert check(size=n, **args) == 0 and check(size=n - 1, **args) == -9
     assert lg.gemm_moe_workspace(0, m) >= 0
