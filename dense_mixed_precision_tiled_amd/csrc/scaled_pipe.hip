@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p
     for (int t = 0; t < nk; ++t) {
         if (t + STAGES - 2 < nk) wait_vmcnt<(STAGES - 2) * NI>();
         else wait_vmcnt<0>();
+        // this wave's reads of tile t - 1, whose stage is loaded next, are done
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
