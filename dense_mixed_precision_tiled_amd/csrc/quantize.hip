@@ -229,21 +229,26 @@ int gemm_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int in_
     if (st != GEMM_OK) return st;
     if (M == 0) return GEMM_OK;
     QuantParams p{};
-    p.X = static_cast<const uint8_t *>(X);
-    p.Q = static_cast<uint8_t *>(Q);
-    p.scales = scales;
     p.ldx = ldx;
     p.ldq = ldq;
-    p.M = (int)M;
     p.K = (int)K;
     const int es = in_dtype == GEMM_F32 ? 4 : 2;
     const bool aligned = (uintptr_t)X % 16 == 0 && (uintptr_t)Q % 16 == 0 &&
                          (ldx * es) % 16 == 0 && ldq % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = in_dtype == GEMM_F32   ? launch_quantize<DT_F32>(p, aligned, s)
-                         : in_dtype == GEMM_F16 ? launch_quantize<DT_F16>(p, aligned, s)
-                                                : launch_quantize<DT_BF16>(p, aligned, s);
-    return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+    // a grid holds fewer than 2^32 threads: 2^21 rows for each launch
+    const int64_t most = (int64_t)1 << 21;
+    for (int64_t i = 0; i < M; i += most) {
+        p.X = static_cast<const uint8_t *>(X) + i * ldx * es;
+        p.Q = static_cast<uint8_t *>(Q) + i * ldq;
+        p.scales = scales + i;
+        p.M = (int)(M - i < most ? M - i : most);
+        const hipError_t e = in_dtype == GEMM_F32   ? launch_quantize<DT_F32>(p, aligned, s)
+                             : in_dtype == GEMM_F16 ? launch_quantize<DT_F16>(p, aligned, s)
+                                                    : launch_quantize<DT_BF16>(p, aligned, s);
+        if (e != hipSuccess) return GEMM_ERR_HIP;
+    }
+    return GEMM_OK;
 }
 
 }  // extern "C"

@@ -130,19 +130,24 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
     const bool aligned = K > 0 && (uintptr_t)A % 16 == 0 && (uintptr_t)B % 16 == 0 &&
                          lda % 16 == 0 && ldb % 16 == 0;
     // Buffer loads reach 4 GiB: K-contiguous operands past that are taken in
-    // parts, rows of D by the extent of A and columns by that of B.
+    // parts, rows of D by the extent of A and columns by that of B.  A part has at
+    // most 2^27 rows and columns (a grid holds fewer than 2^32 threads, a tile's
+    // last row an int).
     const int64_t range = ((int64_t)1 << 32) - 16;
     const bool parts = aligned && akc && bkc && lda <= range / 512 && ldb <= range / 512;
-    const int64_t rows = parts && (M - 1) * lda + K > range ? (range - K) / lda / 256 * 256 : M;
-    const int64_t cols = parts && (N - 1) * ldb + K > range ? (range - K) / ldb / 256 * 256 : N;
+    const int64_t most = (int64_t)1 << 27;
+    int64_t rows = M < most ? M : most, cols = N < most ? N : most;
+    if (parts && (rows - 1) * lda + K > range) rows = (range - K) / lda / 256 * 256;
+    if (parts && (cols - 1) * ldb + K > range) cols = (range - K) / ldb / 256 * 256;
+    const int64_t a_row = akc ? lda : 1, b_col = bkc ? ldb : 1;
     const int osz = out_size(out_dtype);
     for (int64_t i = 0; i < M; i += rows) {
         for (int64_t j = 0; j < N; j += cols) {
             Params q = p;
             q.M = (int)(M - i < rows ? M - i : rows);
             q.N = (int)(N - j < cols ? N - j : cols);
-            q.A = reinterpret_cast<const uint16_t *>(static_cast<const char *>(A) + i * lda);
-            q.B = reinterpret_cast<const uint16_t *>(static_cast<const char *>(B) + j * ldb);
+            q.A = reinterpret_cast<const uint16_t *>(static_cast<const char *>(A) + i * a_row);
+            q.B = reinterpret_cast<const uint16_t *>(static_cast<const char *>(B) + j * b_col);
             if (C)
                 q.C = static_cast<const char *>(C) +
                       (p.c_col ? j * p.ldc + i : i * p.ldc + j) * osz;

@@ -343,9 +343,9 @@ int gemm_validate_ex(int64_t M, int64_t N, int64_t K,
  * An int8 product with a scale for each row of A (a token) and each column of
  * D (an output channel), and the operator that makes such an A from 16-bit or
  * 32-bit activations.  Both enqueue one kernel (gemm_run_scaled one for every
- * 4 GiB of A and of B), allocate nothing and use no workspace, so they can be
- * captured into a HIP graph, and calls on different streams do not touch each
- * other.
+ * 4 GiB of A and of B and every 2^27 rows and columns, gemm_quantize_rows one for
+ * every 2^21 rows), allocate nothing and use no workspace, so they can be captured
+ * into a HIP graph, and calls on different streams do not touch each other.
  *
  * gemm_quantize_rows: for each row i of X (M x K, row-major, ldx >= K),
  *

@@ -202,6 +202,24 @@ def test_operand_past_4_gib(M):
     assert ((D[:, cols].double().cpu() - ref).abs() <= 4 * 2.0 ** -24 * (ref.abs() + 8)).all()
 
 
+@pytest.mark.parametrize("swap", [False, True])
+def test_longest_line(swap):
+    """2^31 - 1 outputs of one row or one column, from one product each."""
+    n = 2 ** 31 - 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    long = torch.randint(-128, 128, (n,), dtype=torch.int8, device="cuda", generator=g)
+    one = torch.tensor([-7], dtype=torch.int8, device="cuda")
+    D = torch.zeros(n + 1, dtype=torch.float16, device="cuda")
+    M, N, A, B = (n, 1, long, one) if swap else (1, n, one, long)
+    log("case: scaled %d x %d x 1" % (M, N))
+    st = lg.gemm_run_scaled(M, N, 1, A.data_ptr(), 1, R, B.data_ptr(), 1, C, 0, 0, 0, N,
+                            D.data_ptr(), N, lg.GEMM_I8, lg.GEMM_I32, F16, 0, None, stream())
+    assert st == 0 and D[n] == 0
+    for i in range(0, n, 2 ** 28):
+        part = long[i:i + 2 ** 28]
+        assert torch.equal(D[i:i + part.numel()], part.to(torch.float16) * -7), i
+
+
 @pytest.mark.parametrize("la,lb", LAYOUTS)
 def test_medium_tiles(la, lb):
     Scaled(1500, 1600, 384, la, lb, out=BF16, bias=True).check("medium")
@@ -373,6 +391,21 @@ def test_quantize_special_rows(dtype):
             assert np.isnan(s[i]) and (Q[i] == 0).all(), i
         else:
             assert np.array_equal(Q[i], q[i]) and s[i] == t[i], i
+
+
+def test_quantize_more_rows_than_a_grid_holds():
+    """2^24 + 3 rows of one value, element by element: 2^32 threads and more."""
+    M = 2 ** 24 + 3
+    g = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(M, generator=g, device="cuda").half()
+    X[::1000] = 0
+    Q = torch.full((M + 1,), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M + 1,), -1.0, device="cuda")
+    st = lg.gemm_quantize_rows(M, 1, X.data_ptr(), 1, F16, Q.data_ptr(), 1, s.data_ptr(), stream())
+    assert st == 0
+    assert Q[M] == 77 and s[M] == -1.0
+    assert torch.equal(Q[:M], (X.sign() * 127).to(torch.int8))
+    assert torch.equal(s[:M].double(), (X.double().abs() / 127).float().double())
 
 
 def test_quantize_without_columns():
