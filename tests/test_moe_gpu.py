@@ -254,6 +254,19 @@ def test_masked_logits(T, E, topk):
         assert (got[1] == 0).all() and np.isnan(got[2:5]).all()
 
 
+@pytest.mark.parametrize("T", [2, 7, 40])
+def test_a_token_that_is_nan_leaves_the_others_alone(T):
+    """Tokens of one expert share matrix instructions, not values."""
+    m = Moe(T, 256, 96, 4, 2, seed=8)
+    ref, tol = m.reference()
+    m.X[1, 5] = float("nan")
+    m.device().call()
+    got = m.result()
+    assert np.isnan(got[1]).all()
+    rest = [t for t in range(T) if t != 1]
+    assert (np.abs(got[rest] - ref[rest]) <= tol[rest]).all()
+
+
 def test_all_tokens_choose_the_same_expert():
     for T in (1, 16, 33, 64):
         for topk, E in ((1, 64), (2, 500)):
