@@ -6,8 +6,10 @@
 namespace libgemm {
 hipError_t launch_large_dma16_i8s(const Params &p, int, int akc, int bkc, dim3 grid,
                                   hipStream_t s) {
-    // the host sends no other layout here
-    if (!akc || !bkc) return hipErrorInvalidValue;
-    return launch_dma_one<CfgLargeDmaI8_16, IT_I8S, true, true>(p, grid, s);
+    using CF = CfgLargeDmaI8_16;
+    // the host sends no other layout, alignment or K here
+    if (!akc || !bkc || !p.vec_ok || p.K % CF::BK != 0) return hipErrorInvalidValue;
+    return launch_params(gemm_dma_kernel<CF, IT_I8S, true, true, false>, grid, dim3(CF::THREADS), p,
+                         s);
 }
 }  // namespace libgemm

@@ -27,8 +27,11 @@ template <int BM, int BN, int WM, int WN, int WK, int STAGES, bool RAGGED>
 __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p) {
     constexpr int BK = 128, MF = 32, KS = 4, NW = WM * WN * WK;
     constexpr int TM = BM / WM / MF, TN = BN / WN / MF;
-    using DA = DmaOperand<BM, BK, NW, MF, true, RAGGED, 1>;
-    using DB = DmaOperand<BN, BK, NW, MF, true, RAGGED, 1>;
+    // A ragged last K-tile is loaded like any other: what lies past K are bytes of the
+    // operand's own lines, or zeros past its end, and as no int8 value is Inf or NaN,
+    // zeros in A's tile alone take them out of the sums.
+    using DA = DmaOperand<BM, BK, NW, MF, true, false, 1>;
+    using DB = DmaOperand<BN, BK, NW, MF, true, false, 1>;
     constexpr int SA = DA::BYTES, SB = DB::BYTES, NI = DA::NI + DB::NI;
     static_assert((STAGES - 2) * NI < 64, "the wait counter holds 63 loads");
     static_assert(KS % WK == 0, "MFMA steps of a K-tile");
@@ -108,7 +111,6 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p
         if constexpr (RAGGED) {
             if (t == nk - 1) {
                 DA::zero_tail(at, p.K - t * BK, tid, 64 * NW);
-                DB::zero_tail(at + SA, p.K - t * BK, tid, 64 * NW);
                 __syncthreads();
             }
         }
