@@ -19,11 +19,14 @@ namespace libgemm {
 // 64 x 64 tile (32 -> 16 KiB for a K-tile), and the MFMAs of a step do not wait
 // for each other.
 //
-// Iteration t: wait until this wave's loads of tile t have landed (those of the
-// STAGES - 2 tiles after it may still be in flight; loads complete in order),
-// barrier (so have the other waves', and all have read tile t - 1), load tile
-// t + STAGES - 1 into tile t - 1's stage, multiply tile t.
-template <int BM, int BN, int WM, int WN, int WK, int STAGES, bool RAGGED>
+// Iteration over G tiles from t on: wait until this wave's loads of them have landed
+// (those of the STAGES - 2 G tiles after them may still be in flight; loads complete
+// in order), barrier (so have the other waves', and all have read the G tiles
+// before), load G tiles into the stages of those, multiply.  G = 2 where a wave has a
+// single MFMA for each tile: barrier and LDS latency are paid half as often (40 x 4096 x
+// 16384: 24.6 -> 20.6 us; 64 rows 23.5 -> 23.1).  More stages than these change
+// nothing (18 of 32 x 32: 23.2).
+template <int BM, int BN, int WM, int WN, int WK, int STAGES, int G, bool RAGGED>
 __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p) {
     constexpr int BK = 128, MF = 32, KS = 4, NW = WM * WN * WK;
     constexpr int TM = BM / WM / MF, TN = BN / WN / MF;
@@ -33,7 +36,8 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p
     using DA = DmaOperand<BM, BK, NW, MF, true, false, 1>;
     using DB = DmaOperand<BN, BK, NW, MF, true, false, 1>;
     constexpr int SA = DA::BYTES, SB = DB::BYTES, NI = DA::NI + DB::NI;
-    static_assert((STAGES - 2) * NI < 64, "the wait counter holds 63 loads");
+    static_assert((STAGES - 2 * G) * NI < 64, "the wait counter holds 63 loads");
+    static_assert(STAGES % G == 0 && STAGES >= 3 * G, "whole groups of stages");
     static_assert(KS % WK == 0, "MFMA steps of a K-tile");
 
     // the end: the TM x TN MFMA tiles that WK waves hold partial sums of are
@@ -96,48 +100,55 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p
     });
     const int nk = (p.K + BK - 1) / BK;
 #pragma nounroll
-    for (int t = 0; t < STAGES - 1 && t < nk; ++t) fetch(t, t);
+    for (int t = 0; t < STAGES - G && t < nk; ++t) fetch(t, t);
     int stage = 0;
 #pragma nounroll
-    for (int t = 0; t < nk; ++t) {
-        if (t + STAGES - 2 < nk) wait_vmcnt<(STAGES - 2) * NI>();
+    for (int t = 0; t < nk; t += G) {
+        if (t + STAGES - G <= nk) wait_vmcnt<(STAGES - 2 * G) * NI>();
         else wait_vmcnt<0>();
-        // this wave's reads of tile t - 1, whose stage is loaded next, are done
+        // this wave's reads of the tiles before, whose stages are loaded next, are done
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         char *const at = lds + stage * (SA + SB);
         if constexpr (RAGGED) {
-            if (t == nk - 1) {
-                DA::zero_tail(at, p.K - t * BK, tid, 64 * NW);
+            if (t + G >= nk) {
+                DA::zero_tail(at + (nk - 1 - t) * (SA + SB), p.K - (nk - 1) * BK, tid, 64 * NW);
                 __syncthreads();
             }
         }
-        u32x4 fa[KS / WK][TM], fb[KS / WK][TN];
-        Unroll<0, KS / WK>::run([&](auto ss) {
+        u32x4 fa[G * KS / WK][TM], fb[G * KS / WK][TN];
+        Unroll<0, G * KS / WK>::run([&](auto ss) {
             constexpr int s = decltype(ss)::value;
-            constexpr uint32_t kx = (uint32_t)(s * WK * 2 * 16);
+            constexpr uint32_t kx = (uint32_t)(s % (KS / WK) * WK * 2 * 16);
+            char *const from = at + s / (KS / WK) * (SA + SB);
             Unroll<0, TM>::run([&](auto ii) {
                 constexpr int i = decltype(ii)::value;
-                fa[s][i] = *reinterpret_cast<const u32x4 *>(at + (a_off[i] ^ kx));
+                fa[s][i] = *reinterpret_cast<const u32x4 *>(from + (a_off[i] ^ kx));
             });
             Unroll<0, TN>::run([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
-                fb[s][j] = *reinterpret_cast<const u32x4 *>(at + (b_off[j] ^ kx));
+                fb[s][j] = *reinterpret_cast<const u32x4 *>(from + (b_off[j] ^ kx));
             });
         });
-        if (t + STAGES - 1 < nk) fetch(t + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-        Unroll<0, KS / WK>::run([&](auto ss) {
+        const int behind = stage == 0 ? STAGES - G : stage - G;
+        Unroll<0, G>::run([&](auto uu) {
+            constexpr int u = decltype(uu)::value;
+            if (t + STAGES - G + u < nk) fetch(t + STAGES - G + u, behind + u);
+        });
+        Unroll<0, G * KS / WK>::run([&](auto ss) {
+            constexpr int s = decltype(ss)::value;
+            // (past the last tile a stage holds anything)
+            if (s / (KS / WK) > 0 && t + s / (KS / WK) >= nk) return;
             Unroll<0, TM>::run([&](auto ii) {
                 Unroll<0, TN>::run([&](auto jj) {
-                    constexpr int s = decltype(ss)::value;
                     constexpr int i = decltype(ii)::value, j = decltype(jj)::value;
                     acc[i][j] = mfma32_1<IT_I8S>(fb[s][j], fa[s][i], acc[i][j]);
                 });
             });
         });
-        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        stage = stage == STAGES - G ? 0 : stage + G;
     }
     __syncthreads();  // every wave has read the last tile: LDS is free
 
@@ -188,16 +199,16 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) scaled_pipe_kernel(Params p
     ScaledEpilogue<CE, (int)sizeof(smem), false>(p, m0, n0, smem, etid).run(sum);
 }
 
-template <int BM, int BN, int WM, int WN, int WK, int STAGES>
+template <int BM, int BN, int WM, int WN, int WK, int STAGES, int G>
 static hipError_t launch_pipe(const Params &p, hipStream_t s) {
     Params q = p;
     q.tiles_m = (p.M + BM - 1) / BM;
     q.tiles_n = (p.N + BN - 1) / BN;
     const dim3 grid((unsigned)((int64_t)q.tiles_m * q.tiles_n)), block(64 * WM * WN * WK);
     return p.K % 128
-               ? launch_params(scaled_pipe_kernel<BM, BN, WM, WN, WK, STAGES, true>, grid, block,
+               ? launch_params(scaled_pipe_kernel<BM, BN, WM, WN, WK, STAGES, G, true>, grid, block,
                                q, s)
-               : launch_params(scaled_pipe_kernel<BM, BN, WM, WN, WK, STAGES, false>, grid, block,
+               : launch_params(scaled_pipe_kernel<BM, BN, WM, WN, WK, STAGES, G, false>, grid, block,
                                q, s);
 }
 
@@ -225,11 +236,11 @@ bool launch_scaled_pipe(const Params &p, int cus, hipStream_t s, hipError_t *sta
     const struct {
         int bm, bn, cycles;
         launch_t launch;
-    } kTiles[] = {{32, 32, 372, launch_pipe<32, 32, 1, 1, 4, 8>},
-                  {64, 32, 488, launch_pipe<64, 32, 1, 1, 4, 6>},
-                  {64, 64, 604, launch_pipe<64, 64, 1, 1, 4, 4>},
-                  {64, 128, 836, launch_pipe<64, 128, 1, 2, 4, 4>},
-                  {128, 128, 1068, launch_pipe<128, 128, 2, 2, 2, 4>}};
+    } kTiles[] = {{32, 32, 372, launch_pipe<32, 32, 1, 1, 4, 12, 2>},
+                  {64, 32, 488, launch_pipe<64, 32, 1, 1, 4, 8, 2>},
+                  {64, 64, 604, launch_pipe<64, 64, 1, 1, 4, 4, 1>},
+                  {64, 128, 836, launch_pipe<64, 128, 1, 2, 4, 4, 1>},
+                  {128, 128, 1068, launch_pipe<128, 128, 2, 2, 2, 4, 1>}};
     launch_t best = nullptr;
     int64_t least = 0;
     for (const auto &t : kTiles) {
