@@ -525,8 +525,10 @@ hipError_t moe_launch(const MoeParams &p, int cus, hipStream_t s) {
     MoeParams arg = p;
     void *args[] = {&arg};
     // Blocks of 16 columns of every slot: one for each wave where that gives every
-    // CU eight waves, otherwise one for each workgroup.  Then about four workgroups
-    // for each CU; one takes several blocks where there are more.
+    // CU eight waves, otherwise one for each workgroup (7 tokens, 16 experts top 4 of
+    // 4096 x 1000: 64 us with a block for each workgroup, 76 for each wave; 64 tokens,
+    // 32 top 4 of 4096 x 2048 in int8: 211 and 198).  Then about four workgroups for each
+    // CU; one takes several blocks where there are more (198; with two 213, eight 198).
     const int64_t blocks = (p.I + 15) / 16;
     const bool alone = blocks * p.slots >= 8 * (int64_t)cus;
     const int64_t parts = alone ? (blocks + 3) / 4 : blocks;

@@ -3,7 +3,8 @@
 //
 // Bound by memory (a row is read once and held in registers between the
 // maximum and the rounding), so the arithmetic for each value is kept to six
-// instructions for 16-bit inputs.
+// instructions for 16-bit inputs.  Rows of bf16: 4096 x 16384 in 45 us (4.4 TB/s),
+// 2048 x 4096 in 8.2, up to 256 rows of up to 8192 in 3 to 4 (a launch).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -193,6 +194,12 @@ using namespace libgemm_host;
 
 namespace {
 
+// Threads for a row and chunks for a thread, the least that hold the row.  Each rule
+// against the next larger one, us:
+//   64 x 1 up to 1024:    4096 x 512   4.5 (256 x 1: 7.1)
+//   256 x 1 up to 4096:   4096 x 4096 11.7 (256 x 2: 13.8)
+//   256 x 2 up to 8192:   4096 x 8192 21.0 (1024 x 2: 35.5)
+//   1024 x 2 up to 32768: 256 x 16384  5.8, 4096 x 16384 45 (read twice: 29, 115)
 template <int IN>
 hipError_t launch_quantize(const QuantParams &p, bool aligned, hipStream_t s) {
     QuantParams arg = p;
