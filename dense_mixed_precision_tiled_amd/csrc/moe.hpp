@@ -193,8 +193,9 @@ __device__ inline void moe_weights(const MoeParams &p, int t, uint32_t *keys, fl
 // (KW = 4: its four waves split H) or for each wave (KW = 1: no exchange between
 // waves); the last workgroup of a slot (blockIdx.x == gridDim.x - 1) writes the
 // slot's tokens and the weights of token blockIdx.y, blockIdx.y + slots, ...
-// instead.  MT = 1 takes the expert's tokens 16 at a time (or at most four, a
-// shorter pass), MT = 0 (T <= 4) four.
+// instead.  MT = 1 takes the expert's tokens 16 at a time (the last four or eight
+// without exchanges), MT = 0 (T <= 4) four.  One token and 8 experts of 2048 x 1024 in
+// bf16: 16 us (4.2 TB/s); 16 tokens that reach 55 of them: 93 us (4.9 TB/s).
 constexpr int kMoeStaged = 4096;  // logits (or pairs) that are held in LDS
 
 template <int IT, bool W8, int MT, int KW, bool VEC>
@@ -294,8 +295,7 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
         // has to be of.  Rounded to one value, its errors come to as much as y's own
         // rounding (1.41 times that together: 0.0024 against 0.0017 of y's norm for
         // bf16); 16 bits of h, or 22, leave them out.  It costs the second kernel the
-        // reads of h twice: 48 -> 53 us for 16 tokens and experts of 2048 x 1024,
-        // 57 -> 71 for 64 tokens and int8 experts of 4096 x 2048.
+        // reads of h twice (57 -> 71 us for 64 tokens and int8 experts of 4096 x 2048).
         uint8_t *const to = p.h + (int64_t)list[row] * p.ldh * 2;
         moe_store4<IT>(to, c, p.I - c, true, g);
 #pragma unroll
@@ -372,22 +372,24 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
     }
 }
 
-// Workgroup b computes columns [16 b, 16 b + 16) of y.  W waves share the
-// (expert, part of I) units; each adds w * (h D_e^T) to its own copy of y in LDS
-// (16 columns of every token), and the copies are added in order.  TM: the most
-// tokens.  Passes of at most two tokens hold both parts of h in one set of rows,
-// longer ones take a second operand for each of w's; those of up to 12 tokens need
-// no exchanges (10.3 us for one token and 8 experts of 2048 x 1024: 3.3 TB/s).
-template <int IT, bool W8, int TM, int W, bool VEC>
+// Workgroup b computes columns [16 b, 16 b + 16) of y, or with NM = 2 columns [8 b,
+// 8 b + 8).  W waves share the (expert, part of I) units; each adds w * (h D_e^T) to
+// its own copy of y in LDS (the columns of every token), and the copies are added in
+// order.  TM: the most tokens.  Passes of at most two tokens hold both parts of h in one set of rows,
+// longer ones take a second operand for each of w's; those of up to 12 tokens (with
+// blocks of 8 columns, 16) need no exchanges.  64 tokens and 32 int8 experts of 4096 x
+// 2048: 71 us (3.8 TB/s), bound by the conversion of the weights to bf16.
+template <int IT, bool W8, int TM, int W, int NM, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
     constexpr int MT = TM <= 4 ? 0 : 1, ROWS = MT == 0 ? 4 : 16;
-    __shared__ f32x4 y[W][TM][4];
+    typedef float Cols __attribute__((ext_vector_type(NM)));
+    __shared__ Cols y[W][TM][4];
     __shared__ int active[kMoeMaxExperts], count[kMoeMaxExperts], expert[kMoeMaxExperts], found;
     __shared__ int pairs[kMoeStaged];
     __shared__ float weight[kMoeMaxTokens * kMoeMaxTopk];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * (4 * NM);
     const bool staged = p.slots * p.T <= kMoeStaged;
 
     // everything that the first kernel found, in one go
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
         if (lane == 0) found = a;
     }
     for (int i = tid; i < W * TM * 4; i += 64 * W)
-        (&y[0][0][0])[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        (&y[0][0][0])[i] = Cols(0.0f);
     __syncthreads();
 
     // parts of I for each expert: enough units for every wave, evenly
@@ -431,23 +433,23 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
         };
         auto hrow = [&](int i) { return (uint32_t)pair(i) * (uint32_t)p.ldh * 2u; };
         StreamRows w[1];
-        w[0].set(lane, p.W2 + ((int64_t)e * p.H + n0) * p.ld2 * S::WES, [&](int i) {
+        w[0].template set<NM>(lane, p.W2 + ((int64_t)e * p.H + n0) * p.ld2 * S::WES, [&](int i) {
             return (uint32_t)min(i, p.H - 1 - n0) * (uint32_t)p.ld2 * S::WES;
         });
         f32x4 s = {1.0f, 1.0f, 1.0f, 1.0f};
         if constexpr (W8) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                s[q] = p.s2[(int64_t)e * p.H + min(n0 + 4 * lg + q, p.H - 1)];
+            for (int q = 0; q < NM; ++q)
+                s[q] = p.s2[(int64_t)e * p.H + min(n0 + NM * lg + q, p.H - 1)];
         }
-        // add row i's sums v of columns 4 lg + 0 .. 3
+        // add row i's sums v of columns NM lg + 0 .. NM - 1
         auto add = [&](int i, const f32x4 &v) {
             const int at = pair(i);
             const float wt = weight[at];
-            f32x4 *dst = &y[wave][at / p.topk][lg];
-            f32x4 o = *dst;
+            Cols *dst = &y[wave][at / p.topk][lg];
+            Cols o = *dst;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] += wt * (v[q] * s[q]);
+            for (int q = 0; q < NM; ++q) o[q] += wt * (v[q] * s[q]);
             *dst = o;
         };
 #pragma nounroll
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                 constexpr int SETS = decltype(sets)::value;
                 StreamX<SETS> x;
                 x.set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
-                StreamQuads<IT, W8, SETS, 1, SETS == 1, true, VEC, 2> stream;
+                StreamQuads<IT, W8, SETS, 1, SETS == 1, true, VEC, 2, NM> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I);
                 v = stream.template own_sums<0>(lane);
                 row = stream_row<SETS>(lane);
@@ -470,11 +472,11 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                 x.set(lane, p.h, [&](int i) {
                     return hrow(i0 + (i & 1)) + (i & 2 ? (uint32_t)p.h_low() : 0u);
                 });
-                StreamQuads<IT, W8, 1, 1, true, true, VEC> stream;
+                StreamQuads<IT, W8, 1, 1, true, true, VEC, 1, NM> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I);
                 v = stream.template own_sums<0>(lane);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)  // row_ror 8: lane l's neighbour at l ^ 8
+                for (int q = 0; q < NM; ++q)  // row_ror 8: lane l's neighbour at l ^ 8
                     v[q] += __int_as_float(
                         __builtin_amdgcn_mov_dpp(__float_as_int(v[q]), 0x128, 0xf, 0xf, true));
                 row = stream_row<1>(lane);
@@ -485,6 +487,8 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                     quads(std::integral_constant<int, 2>{});
                 } else if (n - i0 <= 12) {
                     quads(std::integral_constant<int, 3>{});
+                } else if constexpr (NM == 2) {
+                    quads(std::integral_constant<int, 4>{});
                 } else {
                     StreamRows x[1];
                     x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
@@ -500,13 +504,13 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     }
     __syncthreads();
     for (int i = tid; i < p.T * 4; i += 64 * W) {
-        const int t = i >> 2, g = i & 3, c = n0 + 4 * g;
+        const int t = i >> 2, g = i & 3, c = n0 + NM * g;
         if (c >= p.H) continue;
-        f32x4 v = y[0][t][g];
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int z = 1; z < W; ++z) {
+        for (int z = 0; z < W; ++z) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] += y[z][t][g][q];
+            for (int q = 0; q < NM; ++q) v[q] += y[z][t][g][q];
         }
         // a token whose weights are NaN has a NaN row, also where no expert was
         // chosen
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
         }
         uint8_t *row = p.D + (int64_t)t * p.ldd * 2;
         const bool vec = (reinterpret_cast<uintptr_t>(p.D) % 8 == 0) && p.ldd % 4 == 0;
-        moe_store4<IT>(row, c, p.H - c, vec, v);
+        moe_store4<IT>(row, c, min(p.H - c, NM), vec, v);
     }
 }
 
@@ -534,7 +538,12 @@ hipError_t moe_launch(const MoeParams &p, int cus, hipStream_t s) {
     const int64_t parts = alone ? (blocks + 3) / 4 : blocks;
     const int64_t want = (4 * (int64_t)cus + p.slots - 1) / p.slots;
     const dim3 up((unsigned)(parts < want ? parts : want) + 1, (unsigned)p.slots);
-    const dim3 down((unsigned)((p.H + 15) / 16));
+    // Columns of y in blocks of 16, or of 8 where those of 16 leave half of the CUs idle
+    // (H = 2048, 64 experts top 8: both kernels 147.7 -> 136.6 us at 16 tokens, 27.3 ->
+    // 26.1 at one).  Every block reads all of h, so at H = 4096 those of 8 lose: 7 tokens
+    // 64.2 -> 65.9 us, 64 tokens 198 -> 229.
+    const bool narrow = 2 * ((p.H + 15) / 16) <= cus;
+    const dim3 down((unsigned)(narrow ? (p.H + 7) / 8 : (p.H + 15) / 16));
     const void *k1, *k2;
     if (p.T <= 4)
         k1 = alone ? (const void *)moe_up_kernel<IT, W8, 0, 1, VEC>
@@ -542,9 +551,14 @@ hipError_t moe_launch(const MoeParams &p, int cus, hipStream_t s) {
     else
         k1 = alone ? (const void *)moe_up_kernel<IT, W8, 1, 1, VEC>
                    : (const void *)moe_up_kernel<IT, W8, 1, 4, VEC>;
-    k2 = p.T <= 4    ? (const void *)moe_down_kernel<IT, W8, 4, 8, VEC>
-         : p.T <= 16 ? (const void *)moe_down_kernel<IT, W8, 16, 8, VEC>
-                     : (const void *)moe_down_kernel<IT, W8, 64, 8, VEC>;
+    if (narrow)
+        k2 = p.T <= 4    ? (const void *)moe_down_kernel<IT, W8, 4, 8, 2, VEC>
+             : p.T <= 16 ? (const void *)moe_down_kernel<IT, W8, 16, 8, 2, VEC>
+                         : (const void *)moe_down_kernel<IT, W8, 64, 8, 2, VEC>;
+    else
+        k2 = p.T <= 4    ? (const void *)moe_down_kernel<IT, W8, 4, 8, 4, VEC>
+             : p.T <= 16 ? (const void *)moe_down_kernel<IT, W8, 16, 8, 4, VEC>
+                         : (const void *)moe_down_kernel<IT, W8, 64, 8, 4, VEC>;
     const hipError_t st = hipLaunchKernel(k1, up, dim3(256), args, 0, s);
     if (st != hipSuccess) return st;
     return hipLaunchKernel(k2, down, dim3(512), args, 0, s);

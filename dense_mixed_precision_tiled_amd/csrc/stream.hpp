@@ -159,21 +159,22 @@ __device__ __forceinline__ void stream_transpose(u32x4 (&v)[4], int lane) {
     });
 }
 
-// 16 rows of an operand as a lane reads them: the byte offsets of the four rows of its
-// quad from a common start.  The start is a scalar that moves along K, so the
+// 16 rows of an operand (NM = 2: 8 rows) as a lane reads them: the byte offsets of the
+// four (two) rows of its quad from a common start.  The start is a scalar that moves along K, so the
 // loads need no vector arithmetic for their addresses.
 struct StreamRows {
     const uint8_t *base;
     int64_t low;  // of x in two parts: bytes from the first one to the second
     uint32_t o0, o1, o2, o3;
     // row(i): byte offset of row i
-    template <class F>
+    template <int NM = 4, class F>
     __device__ __forceinline__ void set(int lane, const uint8_t *start, F &&row,
                                         int64_t second = 0) {
-        const int i = lane & 12;
+        const int i = (lane & 12) / (4 / NM);
         base = start;
         low = second;
-        o0 = row(i), o1 = row(i + 1), o2 = row(i + 2), o3 = row(i + 3);
+        o0 = row(i), o1 = row(i + 1);
+        if constexpr (NM == 4) o2 = row(i + 2), o3 = row(i + 3);
     }
     template <int M>
     __device__ __forceinline__ uint32_t quad() const {
@@ -207,20 +208,21 @@ __device__ __forceinline__ u32x4 stream_load(const uint8_t *base, uint32_t offse
 // The sums over groups [gbeg, gend) of K (KG values each) of NF times 16 rows of w
 // and 4 SETS rows of x.  XV, WV: the rows allow 16-byte loads.  DB: a group is in
 // flight while the one before it is multiplied.  XP = 2: x is the sum of two matrices
-// of its type (a value and what its rounding left).
-template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV, int XP = 1>
+// of its type (a value and what its rounding left).  NM = 2: 8 rows of w for each of
+// NF instead of 16.
+template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV, int XP = 1, int NM = 4>
 struct StreamQuads {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
-    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][SETS][XP * XC];
-    f32x4 acc[NF][4][SETS];  // [channel group][row of the quad][row set]
+    u32x4 wv[DB ? 2 : 1][NF][NM], xv[DB ? 2 : 1][SETS][XP * XC];
+    f32x4 acc[NF][NM][SETS];  // [channel group][row of the quad][row set]
 
     // a group that lies below K
     template <int SL>
     __device__ __forceinline__ void load(const StreamRows (&w)[NF], const StreamX<SETS> &x,
                                          int lane, int g) {
         const uint32_t o = (lane >> 4) * 64 + (lane & 3) * 16;
-        Unroll<0, 4>::run([&](auto mm) {
+        Unroll<0, NM>::run([&](auto mm) {
             constexpr int m = decltype(mm)::value;
             Unroll<0, NF>::run([&](auto ff) {
                 constexpr int f = decltype(ff)::value;
@@ -241,7 +243,7 @@ struct StreamQuads {
     __device__ __forceinline__ void load_some(const StreamRows (&w)[NF], const StreamX<SETS> &x,
                                               int lane, int g, int K) {
         const int k = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * S::EPC;
-        Unroll<0, 4>::run([&](auto mm) {
+        Unroll<0, NM>::run([&](auto mm) {
             constexpr int m = decltype(mm)::value;
             Unroll<0, NF>::run([&](auto ff) {
                 constexpr int f = decltype(ff)::value;
@@ -265,7 +267,7 @@ struct StreamQuads {
                 [&](auto hh) { arrive(xv[SL][decltype(ss)::value][decltype(hh)::value]); });
         });
         Unroll<0, NF>::run([&](auto ff) {
-            Unroll<0, 4>::run([&](auto mm) {
+            Unroll<0, NM>::run([&](auto mm) {
                 constexpr int f = decltype(ff)::value, m = decltype(mm)::value;
                 arrive(wv[SL][f][m]);
                 const u32x4 v = wv[SL][f][m];
@@ -289,9 +291,9 @@ struct StreamQuads {
     }
     __device__ __forceinline__ void run(const StreamRows (&w)[NF], const StreamX<SETS> &x,
                                         int lane, int gbeg, int gend, int K) {
-        Unroll<0, NF * 4 * SETS>::run([&](auto ii) {
+        Unroll<0, NF * NM * SETS>::run([&](auto ii) {
             constexpr int i = decltype(ii)::value;
-            acc[i / SETS / 4][i / SETS % 4][i % SETS] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[i / SETS / NM][i / SETS % NM][i % SETS] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         });
         int g = gbeg;
         if constexpr (XV && WV) {
@@ -328,11 +330,11 @@ struct StreamQuads {
         }
     }
     // The sums of channel group f and row set s: row 4 s + (lane % 16) / 4 of x,
-    // channels 4 (lane / 16) + 0 .. 3 (the lanes of a quad hold the same).
+    // channels NM (lane / 16) + 0 .. NM - 1 (the lanes of a quad hold the same).
     template <int f, int s>
     __device__ __forceinline__ f32x4 sums(int lane) const {
-        f32x4 out;
-        Unroll<0, 4>::run([&](auto mm) {
+        f32x4 out = {0.0f, 0.0f, 0.0f, 0.0f};
+        Unroll<0, NM>::run([&](auto mm) {
             constexpr int m = decltype(mm)::value;
             const f32x4 a = acc[f][m][s];
             const float v01 = lane & 1 ? a[1] : a[0], v23 = lane & 1 ? a[3] : a[2];

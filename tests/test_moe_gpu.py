@@ -193,6 +193,15 @@ def test_sizes_and_types(size, x, i8, pad):
     Moe(*size, x=x, i8=i8, pad=pad).check()
 
 
+@pytest.mark.parametrize("size", [(3, 4100, 72, 4, 2), (12, 4097, 100, 3, 1), (40, 4104, 136, 3, 2),
+                                  (64, 4112, 40, 4, 1), (20, 2048, 300, 2, 1), (15, 2000, 64, 1, 1)])
+@pytest.mark.parametrize("x,i8", TYPES)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_wide_layers(size, x, i8, pad):
+    """More columns than blocks of 8 for every CU, and just fewer."""
+    Moe(*size, x=x, i8=i8, pad=pad).check()
+
+
 @pytest.mark.parametrize("act", [SILU, GELU, RELU])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("x,i8", TYPES)

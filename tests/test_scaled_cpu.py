@@ -55,6 +55,13 @@ def quant(M=4, K=40, X=A0, ldx=40, i=lg.GEMM_F16, Q=B0, ldq=48, s=SA):
     return lg.gemm_validate_quantize_rows(M, K, X, ldx, i, Q, ldq, s)
 
 
+def test_silu_is_for_the_experts_layer_only():
+    epi = lg.GemmEpilogue(activation=lg.GEMM_ACT_SILU)
+    assert scaled(epi=epi) == -4
+    assert lg.gemm_validate_ex(8, 6, 32, A0, 32, R, B0, 32, C, None, 6, D0, 6, lg.GEMM_F16,
+                               lg.GEMM_F32, lg.GEMM_F32, epi) == -4
+
+
 def test_quantize_accepts():
     for t in (lg.GEMM_F16, lg.GEMM_BF16, lg.GEMM_F32):
         assert quant(i=t) == 0
