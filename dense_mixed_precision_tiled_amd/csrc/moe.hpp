@@ -199,7 +199,7 @@ __device__ inline void moe_weights(const MoeParams &p, int t, uint32_t *keys, fl
 constexpr int kMoeStaged = 4096;  // logits (or pairs) that are held in LDS
 
 template <int IT, bool W8, int MT, int KW, bool VEC>
-__global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
+__global__ void __launch_bounds__(256, 2) moe_up_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
     __shared__ uint32_t keys[kMoeStaged];
     __shared__ float part[8];
@@ -323,9 +323,10 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
                 constexpr int SETS = decltype(sets)::value;
                 StreamX<SETS> x;
                 x.set(lane, p.X, [&](int i) { return token(n0 + i); });
-                // (a second group in flight takes registers that MT = 0 has better use
-                // for: 27.3 -> 26.9 us for a layer of one token; 149 -> 142 us at 16)
-                StreamQuads<IT, W8, SETS, 2, (MT > 0 && SETS == 1), VEC, VEC> stream;
+                // (a second group in flight: 149 -> 142 us for a layer of 16 tokens, 214 ->
+                // 198 with eight tokens for each of 32 int8 experts of 4096 x 2048; with
+                // MT = 0 its registers cost more than it gives, 26.9 -> 27.3 at one token)
+                StreamQuads<IT, W8, SETS, 2, (MT > 0), VEC, VEC> stream;
                 stream.run(w, x, lane, gbeg, gend, p.H);
                 g = stream.template own_sums<0>(lane);
                 u = stream.template own_sums<1>(lane);
@@ -378,7 +379,9 @@ __global__ void __launch_bounds__(256) moe_up_kernel(MoeParams p) {
 // order.  TM: the most tokens.  Passes of at most two tokens hold both parts of h in one set of rows,
 // longer ones take a second operand for each of w's; those of up to 12 tokens (with
 // blocks of 8 columns, 16) need no exchanges.  64 tokens and 32 int8 experts of 4096 x
-// 2048: 71 us (3.8 TB/s), bound by the conversion of the weights to bf16.
+// 2048: 71 us (3.8 TB/s).  Every workgroup reads all of h, twice the bytes of its
+// weights there: 58 us with a single row of h; the conversion of the weights to bf16 is
+// hidden (69 without it).
 template <int IT, bool W8, int TM, int W, int NM, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
