@@ -40,7 +40,8 @@ struct MoeParams {
     int *expert;    // [slots]
     int *pairs;     // [slots][T] token * topk + rank, ascending
     float *weight;  // [T * topk] weight of each pair
-    uint8_t *h;     // [2][T * topk][ldh] in the type of x: the values, and what is left of them
+    uint8_t *h;     // bf16: [2][T * topk][ldh], the values, and what is left of them;
+                    // fp16: [T * topk][ldh] in fp32
     int ldh;
     __host__ __device__ int64_t h_low() const { return (int64_t)T * topk * ldh * 2; }
 };
@@ -296,11 +297,26 @@ __global__ void __launch_bounds__(256, 2) moe_up_kernel(MoeParams p) {
         // rounding (1.41 times that together: 0.0024 against 0.0017 of y's norm for
         // bf16); 16 bits of h, or 22, leave them out.  It costs the second kernel the
         // reads of h twice (57 -> 71 us for 64 tokens and int8 experts of 4096 x 2048).
-        uint8_t *const to = p.h + (int64_t)list[row] * p.ldh * 2;
-        moe_store4<IT>(to, c, p.I - c, true, g);
+        // fp16's range is too small for h and for what is left of it, so there h
+        // stays fp32 until the second kernel splits scaled rows of it (stream.hpp; two
+        // unscaled parts: 64.4 us instead of 65.2 for 7 tokens and 16 experts of 4096 x
+        // 1000, 192 instead of 205 for 64 tokens and 32 int8 experts of 4096 x 2048).
+        uint8_t *const to = p.h + (int64_t)list[row] * p.ldh * (IT == IT_F16 ? 4 : 2);
+        if constexpr (IT == IT_F16) {
+            float *const d = reinterpret_cast<float *>(to) + c;
+            if (p.I - c >= 4) {
+                *reinterpret_cast<f32x4 *>(d) = g;
+            } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) g[q] = moe_rest<IT>(g[q]);
-        moe_store4<IT>(to + p.h_low(), c, p.I - c, true, g);
+                for (int q = 0; q < 3; ++q)
+                    if (q < p.I - c) d[q] = g[q];
+            }
+        } else {
+            moe_store4<IT>(to, c, p.I - c, true, g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] = moe_rest<IT>(g[q]);
+            moe_store4<IT>(to + p.h_low(), c, p.I - c, true, g);
+        }
     };
     const int step = (4 / KW) * (gridDim.x - 1);
 #pragma nounroll
@@ -386,6 +402,7 @@ template <int IT, bool W8, int TM, int W, int NM, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
     using S = StreamTypes<IT, W8>;
     constexpr int MT = TM <= 4 ? 0 : 1, ROWS = MT == 0 ? 4 : 16;
+    constexpr bool XF = IT == IT_F16;  // h is fp32
     typedef float Cols __attribute__((ext_vector_type(NM)));
     __shared__ Cols y[W][TM][4];
     __shared__ int active[kMoeMaxExperts], count[kMoeMaxExperts], expert[kMoeMaxExperts], found;
@@ -434,7 +451,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
             if (staged) return pairs[at];
             return p.pairs[at];
         };
-        auto hrow = [&](int i) { return (uint32_t)pair(i) * (uint32_t)p.ldh * 2u; };
+        auto hrow = [&](int i) { return (uint32_t)pair(i) * (uint32_t)p.ldh * (XF ? 4u : 2u); };
         StreamRows w[1];
         w[0].template set<NM>(lane, p.W2 + ((int64_t)e * p.H + n0) * p.ld2 * S::WES, [&](int i) {
             return (uint32_t)min(i, p.H - 1 - n0) * (uint32_t)p.ld2 * S::WES;
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                 constexpr int SETS = decltype(sets)::value;
                 StreamX<SETS> x;
                 x.set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
-                StreamQuads<IT, W8, SETS, 1, SETS == 1, true, VEC, 2, NM> stream;
+                StreamQuads<IT, W8, SETS, 1, SETS == 1, true, VEC, 2, NM, XF> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I);
                 v = stream.template own_sums<0>(lane);
                 row = stream_row<SETS>(lane);
@@ -473,9 +490,9 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                 // both parts of h in one set: rows 0 and 1 the values, 2 and 3 the rests
                 StreamX<1> x;
                 x.set(lane, p.h, [&](int i) {
-                    return hrow(i0 + (i & 1)) + (i & 2 ? (uint32_t)p.h_low() : 0u);
+                    return hrow(i0 + (i & 1)) + (!XF && (i & 2) ? (uint32_t)p.h_low() : 0u);
                 });
-                StreamQuads<IT, W8, 1, 1, true, true, VEC, 1, NM> stream;
+                StreamQuads<IT, W8, 1, 1, true, true, VEC, 1, NM, XF> stream;
                 stream.run(w, x, lane, gbeg, gend, p.I);
                 v = stream.template own_sums<0>(lane);
 #pragma unroll
@@ -496,7 +513,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p) {
                     StreamRows x[1];
                     x[0].set(lane, p.h, [&](int i) { return hrow(i0 + i); }, p.h_low());
                     f32x4 acc[1][1] = {};
-                    StreamTiles<IT, W8, 1, 1, false, true, VEC, 2> stream;
+                    StreamTiles<IT, W8, 1, 1, false, true, VEC, 2, XF> stream;
                     stream.run(w, x, lane, gbeg, gend, p.I, acc);
                     v = acc[0][0];
                     row = lane & 15;

@@ -55,10 +55,11 @@ struct StreamTypes {
 template <int ES, bool VEC>
 __device__ __forceinline__ u32x4 stream_chunk(const uint8_t *row, int k, int K) {
     constexpr int EPC = 16 / ES;
+    static_assert(VEC || ES <= 2, "rows of fp32 are aligned");
     const int n = min(max(K - k, 0), EPC);
     if constexpr (VEC) {
         const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (int64_t)(n > 0 ? k : 0) * ES);
-        return ES == 2 ? keep_first(v, n) : keep_first_bytes(v, n);
+        return ES == 2 ? keep_first(v, n) : keep_first_bytes(v, n * ES);
     } else {
         u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -205,17 +206,90 @@ __device__ __forceinline__ u32x4 stream_load(const uint8_t *base, uint32_t offse
     return *reinterpret_cast<const u32x4 *>(base + (uint64_t)offset);
 }
 
+// Rows of x held in fp32 under fp16 weights (XF in what follows): a value times its
+// row's scale, a power of two, is the sum of two fp16 values to 22 significant bits,
+// wherever in fp32's range the row lies.  (Unscaled, the second one would end at
+// 2^-24: 11 bits are left of a value of 1e-4, and one past 65504 is Inf.)  The largest
+// value of a row is not known before its last one is read, so the scale follows the
+// largest so far: where a scaled value would reach 2^15, the row is scaled down to
+// [2^9, 2^10) and its sums with it, which is exact.  What is lost is then below 2^-34
+// of the row's largest value so far.  Scales start at 2^126, which the first values
+// above 2^-111 bring down.
+constexpr float kStreamScale0 = 0x1p126f;
+
+// Magnitudes (as bits) from which a scale of these bits gives 2^15 and more: an exponent
+// field of 269 less the scale's, but never past that of Inf.
+__device__ __forceinline__ uint32_t stream_limit(float scale) {
+    return min((269u << 23) - __float_as_uint(scale), 0x7f800000u);
+}
+// 1 / scale
+__device__ __forceinline__ float stream_unscale(float scale) {
+    return __uint_as_float((254u << 23) - __float_as_uint(scale));
+}
+// The largest magnitude of a lane's N chunks of fp32 values, as bits.
+template <int N>
+__device__ __forceinline__ uint32_t stream_largest(const u32x4 (&v)[N], uint32_t below) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) {
+        const uint32_t b = v[i / 4][i % 4] & 0x7fffffffu;
+        m = max(m, b < below ? b : 0u);
+    }
+    return m;
+}
+// A row's new scale after values of largest finite magnitude m (of this lane; the
+// lanes of a row are those that differ in the bits of LANES).  Returns the step of its
+// exponent, 0 where it stays.
+template <int LANES>
+__device__ __forceinline__ int stream_rescale(float &scale, uint32_t m) {
+#pragma unroll
+    for (int b = 1; b < 64; b <<= 1)
+        if (LANES & b) m = max(m, (uint32_t)__shfl_xor((int)m, b));
+    if (m < stream_limit(scale)) return 0;
+    const uint32_t old = __float_as_uint(scale) >> 23, e = 263 - (m >> 23);
+    scale = __uint_as_float(e << 23);
+    return (int)e - (int)old;
+}
+__device__ __forceinline__ void stream_shift(f32x4 &v, int step) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], step);
+}
+// Eight fp32 values times scale as two fp16 parts.  finite: all of them are; otherwise the
+// second parts are 0 (Inf less Inf would be NaN).
+__device__ __forceinline__ void stream_split(const u32x4 &a, const u32x4 &b, float scale,
+                                             bool finite, u32x4 &hi, u32x4 &lo) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const u32x4 &v = i < 2 ? a : b;
+        const float x = __uint_as_float(v[2 * (i & 1)]) * scale;
+        const float y = __uint_as_float(v[2 * (i & 1) + 1]) * scale;
+        const uint32_t both = pack_out16<DT_F16>(x, y);
+        const f16x2 h = __builtin_bit_cast(f16x2, both);
+        hi[i] = both;
+        const uint32_t rest = pack_out16<DT_F16>(x - (float)h[0], y - (float)h[1]);
+        lo[i] = finite ? rest : 0u;
+    }
+}
+
 // The sums over groups [gbeg, gend) of K (KG values each) of NF times 16 rows of w
 // and 4 SETS rows of x.  XV, WV: the rows allow 16-byte loads.  DB: a group is in
 // flight while the one before it is multiplied.  XP = 2: x is the sum of two matrices
-// of its type (a value and what its rounding left).  NM = 2: 8 rows of w for each of
-// NF instead of 16.
-template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV, int XP = 1, int NM = 4>
+// of its type (a value and what its rounding left), or with XF of fp32 rows.  With XF and
+// XP = 1 rows i and i + 2 of a set are the two parts of the same one.  NM = 2: 8 rows
+// of w for each of NF instead of 16.
+template <int XT, bool W8, int SETS, int NF, bool DB, bool XV, bool WV, int XP = 1, int NM = 4,
+          bool XF = false>
 struct StreamQuads {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
-    u32x4 wv[DB ? 2 : 1][NF][NM], xv[DB ? 2 : 1][SETS][XP * XC];
+    static constexpr int XES = XF ? 4 : S::XES;
+    static constexpr int XM = XF ? 2 * XC : XC;  // 16-byte chunks that are next to each other
+    static constexpr int NX = XF ? XM : XP * XC;
+    static_assert(!XF || (XT == IT_F16 && XV), "fp32 rows go with fp16 weights");
+    u32x4 wv[DB ? 2 : 1][NF][NM], xv[DB ? 2 : 1][SETS][NX];
     f32x4 acc[NF][NM][SETS];  // [channel group][row of the quad][row set]
+    float scale[XF ? SETS : 1];
 
     // a group that lies below K
     template <int SL>
@@ -231,11 +305,11 @@ struct StreamQuads {
             });
         });
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XP * XC>::run([&](auto hh) {
+            Unroll<0, NX>::run([&](auto hh) {
                 constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
-                const uint8_t *from = h < XC ? x.base : x.base + x.low;
+                const uint8_t *from = h < XM ? x.base : x.base + x.low;
                 xv[SL][s][h] =
-                    stream_load(from + (int64_t)g * 256 * XC + 16 * (h % XC), x.o[s] + o * XC);
+                    stream_load(from + (int64_t)g * 256 * XM + 16 * (h % XM), x.o[s] + o * XM);
             });
         });
     }
@@ -252,20 +326,50 @@ struct StreamQuads {
             });
         });
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XP * XC>::run([&](auto hh) {
+            Unroll<0, NX>::run([&](auto hh) {
                 constexpr int s = decltype(ss)::value, h = decltype(hh)::value;
-                const uint8_t *from = h < XC ? x.base : x.base + x.low;
-                xv[0][s][h] =
-                    stream_chunk<S::XES, XV>(from + x.o[s], k + h % XC * (16 / S::XES), K);
+                const uint8_t *from = h < XM ? x.base : x.base + x.low;
+                xv[0][s][h] = stream_chunk<XES, XV>(from + x.o[s], k + h % XM * (16 / XES), K);
             });
         });
     }
+    // the fp32 values of set s as fp16 parts, in their place
+    template <int SL, int s>
+    __device__ __forceinline__ void split(int lane) {
+        const uint32_t m = stream_largest(xv[SL][s], ~0u);
+        if (__ballot(m >= stream_limit(scale[s]))) {
+            const int step =
+                stream_rescale<1 + 2 + 16 + 32>(scale[s], stream_largest(xv[SL][s], 0x7f800000u));
+            Unroll<0, NF * NM>::run([&](auto ii) {
+                constexpr int i = decltype(ii)::value;
+                stream_shift(acc[i / NM][i % NM][s], step);
+            });
+        }
+        u32x4 hi[XC], lo[XC];
+        Unroll<0, XC>::run([&](auto cc) {
+            constexpr int c = decltype(cc)::value;
+            stream_split(xv[SL][s][2 * c], xv[SL][s][2 * c + 1], scale[s], m < 0x7f800000u, hi[c],
+                         lo[c]);
+        });
+        Unroll<0, XC>::run([&](auto cc) {
+            constexpr int c = decltype(cc)::value;
+            if constexpr (XP == 2) {
+                xv[SL][s][c] = hi[c];
+                xv[SL][s][XC + c] = lo[c];
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) xv[SL][s][c][d] = lane & 8 ? lo[c][d] : hi[c][d];
+            }
+        });
+    }
     template <int SL>
-    __device__ __forceinline__ void multiply() {
+    __device__ __forceinline__ void multiply(int lane) {
         Unroll<0, SETS>::run([&](auto ss) {
-            Unroll<0, XP * XC>::run(
+            Unroll<0, NX>::run(
                 [&](auto hh) { arrive(xv[SL][decltype(ss)::value][decltype(hh)::value]); });
         });
+        if constexpr (XF)
+            Unroll<0, SETS>::run([&](auto ss) { split<SL, decltype(ss)::value>(lane); });
         Unroll<0, NF>::run([&](auto ff) {
             Unroll<0, NM>::run([&](auto mm) {
                 constexpr int f = decltype(ff)::value, m = decltype(mm)::value;
@@ -295,6 +399,8 @@ struct StreamQuads {
             constexpr int i = decltype(ii)::value;
             acc[i / SETS / NM][i / SETS % NM][i % SETS] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         });
+        if constexpr (XF)
+            Unroll<0, SETS>::run([&](auto ss) { scale[decltype(ss)::value] = kStreamScale0; });
         int g = gbeg;
         if constexpr (XV && WV) {
             const int whole = min(gend, K / S::KG);  // groups that lie below K
@@ -304,29 +410,29 @@ struct StreamQuads {
                 for (; g + 2 <= whole; g += 2) {
                     load<1>(w, x, lane, g + 1);
                     __builtin_amdgcn_sched_barrier(0);
-                    multiply<0>();
+                    multiply<0>(lane);
                     __builtin_amdgcn_sched_barrier(0);
                     if (g + 2 < whole) load<0>(w, x, lane, g + 2);
                     __builtin_amdgcn_sched_barrier(0);
-                    multiply<DB ? 1 : 0>();
+                    multiply<DB ? 1 : 0>(lane);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (g < whole) {
-                    multiply<0>();
+                    multiply<0>(lane);
                     ++g;
                 }
             } else {
 #pragma nounroll
                 for (; g < whole; ++g) {
                     load<0>(w, x, lane, g);
-                    multiply<0>();
+                    multiply<0>(lane);
                 }
             }
         }
 #pragma nounroll
         for (; g < gend; ++g) {
             load_some(w, x, lane, g, K);
-            multiply<0>();
+            multiply<0>(lane);
         }
     }
     // The sums of channel group f and row set s: row 4 s + (lane % 16) / 4 of x,
@@ -345,6 +451,7 @@ struct StreamQuads {
             } else {
                 const float p = __uint_as_float(v) + __uint_as_float(quad_xor<1>(v));
                 out[m] = p + __uint_as_float(quad_xor<2>(__float_as_uint(p)));
+                if constexpr (XF) out[m] *= stream_unscale(scale[s]);
             }
         });
         return out;
@@ -375,17 +482,23 @@ __device__ __forceinline__ int stream_row(int lane) {
 // The same for MT times 16 rows of x, exchanged inside the quads (x and w alike) so
 // that one MFMA serves 16 rows: acc[t][f] += the products of w[f] and x[t].  Lane l
 // of acc holds row l % 16 of x, channels 4 (l / 16) + 0 .. 3.
-template <int XT, bool W8, int MT, int NF, bool DB, bool XV, bool WV, int XP = 1>
+template <int XT, bool W8, int MT, int NF, bool DB, bool XV, bool WV, int XP = 1,
+          bool XF = false>
 struct StreamTiles {
     using S = StreamTypes<XT, W8>;
     static constexpr int XC = S::XC;
-    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][MT][XP * XC][4];
+    static constexpr int XES = XF ? 4 : S::XES;
+    static constexpr int XM = XF ? 2 * XC : XC;  // runs of 64 bytes that are next to each other
+    static constexpr int NX = XF ? XM : XP * XC;
+    static_assert(!XF || (XT == IT_F16 && XV && XP == 2), "fp32 rows as two fp16 parts");
+    u32x4 wv[DB ? 2 : 1][NF][4], xv[DB ? 2 : 1][MT][NX][4];
+    float scale[XF ? MT : 1];
 
     template <int SL>
     __device__ __forceinline__ void load(const StreamRows (&w)[NF], const StreamRows (&x)[MT],
                                          int lane, int g) {
         const uint32_t wo = (lane >> 4) * 64 + (lane & 3) * 16;
-        const uint32_t xo = (lane >> 4) * 64 * XC + (lane & 3) * 16;
+        const uint32_t xo = (lane >> 4) * 64 * XM + (lane & 3) * 16;
         Unroll<0, 4>::run([&](auto mm) {
             constexpr int m = decltype(mm)::value;
             Unroll<0, NF>::run([&](auto ff) {
@@ -394,12 +507,12 @@ struct StreamTiles {
                     stream_load(w[f].base + (int64_t)g * 256, w[f].template quad<m>() + wo);
             });
         });
-        Unroll<0, 4 * XP * XC>::run([&](auto mm) {
+        Unroll<0, 4 * NX>::run([&](auto mm) {
             constexpr int h = decltype(mm)::value / 4, m = decltype(mm)::value % 4;
             Unroll<0, MT>::run([&](auto tt) {
                 constexpr int t = decltype(tt)::value;
-                const uint8_t *from = h < XC ? x[t].base : x[t].base + x[t].low;
-                xv[SL][t][h][m] = stream_load(from + (int64_t)g * 256 * XC + 64 * (h % XC),
+                const uint8_t *from = h < XM ? x[t].base : x[t].base + x[t].low;
+                xv[SL][t][h][m] = stream_load(from + (int64_t)g * 256 * XM + 64 * (h % XM),
                                               x[t].template quad<m>() + xo);
             });
         });
@@ -408,7 +521,7 @@ struct StreamTiles {
     __device__ __forceinline__ void load_some(const StreamRows (&w)[NF], const StreamRows (&x)[MT],
                                               int lane, int g, int K) {
         const int kw = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * S::EPC;
-        const int kx = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * (16 / S::XES);
+        const int kx = g * S::KG + (lane >> 4) * S::KB + (lane & 3) * (16 / XES);
         Unroll<0, 4>::run([&](auto mm) {
             constexpr int m = decltype(mm)::value;
             Unroll<0, NF>::run([&](auto ff) {
@@ -417,24 +530,45 @@ struct StreamTiles {
                     stream_chunk<S::WES, WV>(w[f].base + w[f].template quad<m>(), kw, K);
             });
         });
-        Unroll<0, 4 * XP * XC>::run([&](auto mm) {
+        Unroll<0, 4 * NX>::run([&](auto mm) {
             constexpr int h = decltype(mm)::value / 4, m = decltype(mm)::value % 4;
             Unroll<0, MT>::run([&](auto tt) {
                 constexpr int t = decltype(tt)::value;
-                const uint8_t *from = h < XC ? x[t].base : x[t].base + x[t].low;
-                xv[0][t][h][m] = stream_chunk<S::XES, XV>(from + x[t].template quad<m>(),
-                                                          kx + 64 / S::XES * (h % XC), K);
+                const uint8_t *from = h < XM ? x[t].base : x[t].base + x[t].low;
+                xv[0][t][h][m] = stream_chunk<XES, XV>(from + x[t].template quad<m>(),
+                                                       kx + 64 / XES * (h % XM), K);
             });
+        });
+    }
+    // the fp32 values of row group t (pieces of four, in the order of k) as fp16 parts, in
+    // their place
+    template <int SL, int t>
+    __device__ __forceinline__ void split(f32x4 (&acc)[MT][NF]) {
+        u32x4 v[4 * NX];
+        Unroll<0, 4 * NX>::run([&](auto ii) {
+            v[decltype(ii)::value] = xv[SL][t][decltype(ii)::value / 4][decltype(ii)::value % 4];
+        });
+        const uint32_t m = stream_largest(v, ~0u);
+        if (__ballot(m >= stream_limit(scale[t]))) {
+            const int step = stream_rescale<16 + 32>(scale[t], stream_largest(v, 0x7f800000u));
+            Unroll<0, NF>::run(
+                [&](auto ff) { stream_shift(acc[t][decltype(ff)::value], step); });
+        }
+        Unroll<0, 4 * XC>::run([&](auto cc) {
+            constexpr int c = decltype(cc)::value;
+            stream_split(v[2 * c], v[2 * c + 1], scale[t], m < 0x7f800000u, xv[SL][t][c / 4][c % 4],
+                         xv[SL][t][XC + c / 4][c % 4]);
         });
     }
     template <int SL>
     __device__ __forceinline__ void multiply(f32x4 (&acc)[MT][NF], int lane) {
         Unroll<0, MT>::run([&](auto tt) {
-            Unroll<0, XP * XC>::run([&](auto hh) {
+            Unroll<0, NX>::run([&](auto hh) {
                 constexpr int t = decltype(tt)::value, h = decltype(hh)::value;
                 Unroll<0, 4>::run([&](auto mm) { arrive(xv[SL][t][h][decltype(mm)::value]); });
                 stream_transpose(xv[SL][t][h], lane);
             });
+            if constexpr (XF) split<SL, decltype(tt)::value>(acc);
         });
         Unroll<0, NF>::run([&](auto ff) {
             constexpr int f = decltype(ff)::value;
@@ -466,6 +600,8 @@ struct StreamTiles {
     __device__ __forceinline__ void run(const StreamRows (&w)[NF], const StreamRows (&x)[MT],
                                         int lane, int gbeg, int gend, int K,
                                         f32x4 (&acc)[MT][NF]) {
+        if constexpr (XF)
+            Unroll<0, MT>::run([&](auto tt) { scale[decltype(tt)::value] = kStreamScale0; });
         int g = gbeg;
         if constexpr (XV && WV) {
             const int whole = min(gend, K / S::KG);  // groups that lie below K
@@ -499,6 +635,13 @@ struct StreamTiles {
             load_some(w, x, lane, g, K);
             multiply<0>(acc, lane);
         }
+        if constexpr (XF)
+            Unroll<0, MT * NF>::run([&](auto ii) {
+                constexpr int i = decltype(ii)::value;
+                const float f = stream_unscale(scale[i / NF]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i / NF][i % NF][e] *= f;
+            });
     }
 };
 

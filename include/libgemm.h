@@ -465,9 +465,11 @@ int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
  * logits of its own time.  The same call gives the same bits.
  *
  * Accuracy: products and sums are fp32, as are the softmax and everything
- * between; h is held as the sum of two values of in_dtype (16 significant bits
- * for bf16, 22 for fp16; an fp16 h overflows to Inf past 65504), and y is
- * rounded once at the end.  int8 weights are converted exactly and their scales
+ * between, and y is rounded once at the end.  The second product takes h as the sum
+ * of two values of in_dtype: 16 significant bits for bf16; for fp16 22, of h times a
+ * power of two that follows the largest value of its row (one token and expert), so
+ * that h may lie anywhere in fp32's range, and what is below 2^-34 of the row's
+ * largest value is lost.  int8 weights are converted exactly and their scales
  * applied to the fp32 sums.  An Inf in a chosen expert's W2 gives NaN.
  *
  * Speed: bound by the chosen experts' weights, each read once.  16-byte loads

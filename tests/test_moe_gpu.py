@@ -400,3 +400,77 @@ def test_router_and_layer(x, i8):
     q = np.rint(127 * y / a[:, None])
     P = q @ W.double().cpu().numpy().T * (a / 127)[:, None] * sB.double().cpu().numpy()
     assert (np.abs(out.double().cpu().numpy() - P) <= 8.1 * 2.0 ** -24 * np.abs(P)).all()
+
+
+def rows_close(m, label):
+    """Every token's row by its norm: y's rounding is at most r of it (2^-25 for an
+    element that is subnormal in fp16), and half as much again is left for the rest."""
+    log("case: moe T%d H%d I%d x%d i8 %d pad %d %s" % (m.T, m.H, m.I, m.x, m.i8, m.pad, label))
+    m.device().call()
+    got = m.result()
+    ref, _ = m.reference()
+    assert np.isfinite(got).all(), label
+    err, norm = np.linalg.norm(got - ref, axis=1), np.linalg.norm(ref, axis=1)
+    bound = 1.5 * HALF_STEP[m.x] * norm + 2.0 ** -25 * m.H ** 0.5
+    assert (err <= bound).all(), "%s: rows off by %s of their norm" % (label, (err / norm)[err > bound])
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 7, 20, 50])
+@pytest.mark.parametrize("H", [64, 2200])
+@pytest.mark.parametrize("x,i8", TYPES)
+def test_inner_values_of_any_size(T, H, x, i8):
+    """h far below and above 1, y in the middle of its type's range: fp16 alone could
+    not hold h and what rounding leaves of it.  Small and large tokens side by side."""
+    for size, back in ((1e-1, 1e1), (1e-2, 1e3), (1e-3, 3e3), (300.0, 1e-3), (2000.0, 1e-4)):
+        for pad in (0, 3):
+            m = Moe(T, H, 333, 2, 1, x=x, i8=i8, renorm=True, pad=pad)
+            m.X = (m.X * size).to(m.X.dtype)
+            if i8:
+                m.s2 = m.s2 * back
+            else:
+                m.W2 = (m.W2.float() * back).to(m.W2.dtype)
+            rows_close(m, "x %g" % size)
+    m = Moe(T, H, 333, 2, 1, x=x, i8=i8, renorm=True)
+    m.X = (m.X * torch.logspace(-2, 2, T)[:, None]).to(m.X.dtype)
+    # (y of the largest token's h, about 1e4, stays finite)
+    rows_close(m, "tokens of 1e-2 to 1e2")
+
+
+@pytest.mark.parametrize("T", [1, 3, 12, 50])
+@pytest.mark.parametrize("H", [64, 2200])
+@pytest.mark.parametrize("x,i8", TYPES)
+def test_inner_values_that_grow_along_the_row(T, H, x, i8):
+    """Rows of h that start with zeros or small values and grow, or shrink, over I."""
+    I = 700
+    for name, f in (("grow", torch.logspace(-4, 1, I)), ("shrink", torch.logspace(1, -4, I)),
+                    ("late", torch.cat([torch.zeros(400), torch.full((I - 400,), 1e-2)]))):
+        m = Moe(T, H, I, 2, 1, x=x, i8=i8, renorm=True)
+        if i8:
+            m.s1.view(2, 2, I)[:, 1] *= f
+        else:
+            m.W1.view(2, 2, I, H)[:, 1] *= f[:, None].to(m.W1.dtype)
+        rows_close(m, name)
+
+
+@pytest.mark.parametrize("T", [1, 2, 6, 40])
+@pytest.mark.parametrize("x", [BF16, F16])
+def test_inner_values_over_the_range_of_fp32(T, x):
+    """int8 weights whose scales put h near 1e-24 or 1e22, and y near 1."""
+    for up, down in ((1e-12, 1e24), (1e11, 1e-22)):
+        m = Moe(T, 96, 300, 2, 1, x=x, i8=True, renorm=True)
+        m.s1, m.s2 = m.s1 * up, m.s2 * down
+        rows_close(m, "scales of %g" % up)
+
+
+@pytest.mark.parametrize("T", [2, 7, 40])
+@pytest.mark.parametrize("H", [64, 2200])
+@pytest.mark.parametrize("x,i8", TYPES)
+def test_an_infinite_token_leaves_the_others_alone(T, H, x, i8):
+    """A token whose h is Inf or NaN shares the others' rows of the matrix units."""
+    m = Moe(T, H, 333, 2, 1, x=x, i8=i8, seed=4)
+    ref, tol = m.reference()
+    m.X[0, 5] = float("inf")
+    m.device().call()
+    got = m.result()
+    assert not np.isfinite(got[0]).any()
+    assert (np.abs(got[1:] - ref[1:]) <= tol[1:]).all()
