@@ -481,3 +481,77 @@ def test_linear_layer_in_a_graph(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(b[6], want)
+
+
+# --------------------------------------- the large tiles without C or activation
+@pytest.mark.parametrize("out", [F32, F16, BF16])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("K", [256, 300])
+@pytest.mark.parametrize("M,N", [(3501, 3601), (4203, 4111)])
+def test_large_tiles_without_c(M, N, K, bias, out):
+    """The four-wave tile (K = 256) and the eight-wave one (300), at 14 x 15 tiles and
+    with 17 x 17, more tiles than CUs, in the staggered order; odd edges."""
+    Scaled(M, N, K, out=out, bias=bias).check("large, out %d bias %d" % (out, bias))
+
+
+@pytest.mark.parametrize("la,lb", [(R, R), (C, C), (C, R)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_large_tiles_without_c_in_other_layouts(la, lb, out):
+    Scaled(3501, 3601, 200, la, lb, out=out, bias=True).check("large, A%d B%d" % (la, lb))
+    Scaled(3501, 3601, 72, la, lb, out=out, pad=3).check("large, A%d B%d elements" % (la, lb))
+
+
+@pytest.mark.parametrize("out", [F32, F16, BF16])
+@pytest.mark.parametrize("M,N,K,lb", [(8, 203, 264, C), (40, 500, 200, C), (100, 200, 96, R),
+                                      (3500, 3600, 256, C), (3500, 3600, 300, C)])
+def test_satf_in_every_type(M, N, K, lb, out):
+    """Rows that overflow the output type and one of NaN: with satf the largest finite
+    value and 0, without it Inf and NaN; the rows between them as ever."""
+    p = Scaled(M, N, K, lb=lb, out=out, bias=True)
+    p.sA[2::3] = 1e30 if out == F16 else 3e38
+    p.sA[1] = np.nan
+    top = torch.finfo(TORCH[out]).max
+    rest = np.ones(M, bool)
+    rest[1], rest[2::3] = False, False
+    for satf in (0, 1):
+        p.satf = satf
+        p.device()
+        p.call()
+        got, pad = p.result()
+        log("case: scaled %dx%dx%d satf %d out %d" % (M, N, K, satf, out))
+        with np.errstate(invalid="ignore", over="ignore"):
+            ref, tol = p.reference()
+        assert (np.abs(got[rest] - ref[rest]) <= tol[rest]).all()
+        big, sign = got[2::3], np.sign(ref[2::3])
+        over = np.abs(ref[2::3]) > 2 * top
+        assert over.any()
+        want = sign * (top if satf else np.inf)
+        assert (big[over] == want[over]).all()
+        assert (got[1] == 0).all() if satf else np.isnan(got[1]).all()
+        assert (pad == PADD).all()
+
+
+@pytest.mark.parametrize("swap", [False, True])
+def test_strided_operand_past_4_gib(swap):
+    """A row-major B (or column-major A) of 4.6 GB, read element by element."""
+    N, K, M = 70000, 65536, 3
+    g = torch.Generator(device="cuda").manual_seed(10)
+    few = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    many = torch.randint(-127, 128, (K, N), dtype=torch.int8, device="cuda", generator=g)
+    scale = torch.rand(N, device="cuda", generator=g) + 0.5
+    D = torch.zeros(N, M, device="cuda") if swap else torch.zeros(M, N, device="cuda")
+    log("case: strided operand past 4 GiB, swap %d" % swap)
+    if swap:  # A(i, k) = many[k][i], B(k, j) = few[j][k]
+        st = lg.gemm_run_scaled(N, M, K, many.data_ptr(), N, C, few.data_ptr(), K, C,
+                                scale.data_ptr(), 0, 0, M, D.data_ptr(), M, lg.GEMM_I8, lg.GEMM_I32,
+                                F32, 0, None, stream())
+    else:
+        st = lg.gemm_run_scaled(M, N, K, few.data_ptr(), K, R, many.data_ptr(), N, R, 0,
+                                scale.data_ptr(), 0, N, D.data_ptr(), N, lg.GEMM_I8, lg.GEMM_I32,
+                                F32, 0, None, stream())
+    assert st == 0
+    cols = [0, 1, 30000, 65535, 65536, 69999]
+    ref = (few.double() @ many[:, cols].double()) * scale[cols].double()
+    got = (D.t() if swap else D)[:, cols].double()
+    # the sum's rounding and one multiplication
+    assert ((got - ref).abs() <= 2.02 * 2.0 ** -24 * ref.abs()).all()
