@@ -474,3 +474,88 @@ def test_an_infinite_token_leaves_the_others_alone(T, H, x, i8):
     got = m.result()
     assert not np.isfinite(got[0]).any()
     assert (np.abs(got[1:] - ref[1:]) <= tol[1:]).all()
+
+
+@pytest.mark.parametrize("size", [(4, 64, 1100, 32, 8), (3, 72, 1537, 64, 8), (1, 40, 4100, 8, 8),
+                                  (2, 40, 600, 1024, 32)])
+@pytest.mark.parametrize("x,i8", TYPES)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_few_tokens_of_wide_experts(size, x, i8, pad):
+    """Up to four tokens and a block of columns for each wave of the first kernel."""
+    Moe(*size, x=x, i8=i8, pad=pad).check()
+
+
+@pytest.mark.parametrize("T", [1, 5, 64])
+@pytest.mark.parametrize("x,i8", TYPES)
+def test_most_experts_and_ranks(T, x, i8):
+    """1024 experts, top 32: the limits."""
+    Moe(T, 32, 24, 1024, 32, x=x, i8=i8, renorm=T == 5).check()
+
+
+@pytest.mark.parametrize("x", [BF16, F16])
+def test_longest_lines(x):
+    """Leading dimensions of 2^24 elements: X, D and the weights past 2 GiB, logits past 4."""
+    T, H, I, E, ld = 64, 40, 24, 2, 2 ** 24
+    m = Moe(T, H, I, E, 2, x=x)
+
+    def lines(t):
+        store = torch.full((t.shape[0], ld), float("nan"), dtype=t.dtype, device="cuda")
+        store[:, :t.shape[1]] = t.cuda()
+        return store
+
+    log("case: moe lines of 2^24, x%d" % x)
+    X, W1, W2, logits = lines(m.X), lines(m.W1), lines(m.W2), lines(m.logits)
+    D = torch.full((T, ld), SENTINEL, dtype=TORCH[x], device="cuda")
+    layer = lg.GemmMoe(H, I, E, 2, x, W1.data_ptr(), ld, W2.data_ptr(), ld)
+    ws = torch.empty(lg.gemm_moe_workspace(T, layer), dtype=torch.uint8, device="cuda")
+    st = lg.gemm_moe_run(T, layer, X.data_ptr(), ld, logits.data_ptr(), ld, D.data_ptr(), ld, x,
+                         ws.data_ptr(), ws.numel(), stream())
+    assert st == 0
+    ref, tol = m.reference()
+    assert (np.abs(D[:, :H].double().cpu().numpy() - ref) <= tol).all()
+    assert (D[:, H:H + 64] == SENTINEL).all() and (D[:, ld - 64:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("x", [BF16, F16])
+def test_widest_inner_rows(x):
+    """2048 pairs of 2^19 inner values: 4 GiB of them in the workspace."""
+    T, H, I, E, topk = 64, 8, 2 ** 19, 32, 32
+    t = TORCH[x]
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    X, logits = rand(T, H).to(t), rand(T, E)
+    W1, W2 = (rand(E * 2 * I, H) / H ** 0.5).to(t), (rand(E * H, I) / I ** 0.5).to(t)
+    D = torch.full((T + 1, H), SENTINEL, dtype=t, device="cuda")
+    layer = lg.GemmMoe(H, I, E, topk, x, W1.data_ptr(), H, W2.data_ptr(), I)
+    ws = torch.empty(lg.gemm_moe_workspace(T, layer), dtype=torch.uint8, device="cuda")
+    log("case: moe widest inner rows, x%d, workspace %d" % (x, ws.numel()))
+    st = lg.gemm_moe_run(T, layer, X.data_ptr(), H, logits.data_ptr(), E, D.data_ptr(), H, x,
+                         ws.data_ptr(), ws.numel(), stream())
+    assert st == 0
+    w = torch.softmax(logits.double(), 1)
+    ref = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        w1 = W1[e * 2 * I:(e + 1) * 2 * I].double()
+        gate, up = X.double() @ w1[:I].t(), X.double() @ w1[I:].t()
+        h = gate * torch.sigmoid(gate) * up
+        ref += w[:, e:e + 1] * (h @ W2[e * H:(e + 1) * H].double().t())
+    assert (D[T] == SENTINEL).all()
+    # y's rounding, and as much again for sums of 2^19 terms of either sign
+    err = torch.linalg.norm(D[:T].double() - ref, dim=1) / torch.linalg.norm(ref, dim=1)
+    assert (err <= 2 * HALF_STEP[x]).all(), err.max().item()
+
+
+@pytest.mark.parametrize("x,i8", TYPES)
+@pytest.mark.parametrize("offset", [1, 100, 255])
+def test_workspace_at_any_address(x, i8, offset):
+    """The size that gemm_moe_workspace names is enough wherever the memory starts."""
+    m = Moe(20, 96, 72, 8, 2, x=x, i8=i8).device()
+    m.call()
+    want = m.dD.clone()
+    size = m.ws.numel()
+    store = torch.full((offset + size + 64,), 99, dtype=torch.uint8, device="cuda")
+    m.ws = store[offset:offset + size]
+    m.dD.fill_(SENTINEL)
+    m.call()
+    assert torch.equal(m.dD, want)
+    assert (store[:offset] == 99).all() and (store[offset + size:] == 99).all()
