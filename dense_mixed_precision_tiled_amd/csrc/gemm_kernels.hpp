@@ -1915,8 +1915,11 @@ __device__ __forceinline__ float gelu_select(float x) {
 // segments (256 bytes of 16-bit outputs at 128 columns) instead of 8 bytes in
 // each of 16 rows.  (In registers, as tile_epilogue finishes interior tiles, the
 // scales of a lane's rows and columns and the three output types made the
-// eight-wave kernels spill 100 to 550 registers.)  Row values are staged in LDS
-// as well: a load from memory between two stores waits for both.
+// eight-wave kernels spill 100 to 550 registers.  Staged, those with vector loads of
+// K-contiguous operands spill none, of other layouts 3 to 11; with element loads they
+// still spill 97 to 163.)  Row values are staged in LDS as well: a load from memory
+// between two stores waits for both.  C is loaded element by element: 4096^3 in bf16
+// takes 117 us with C, 84 with GELU and 74 with neither.
 //
 // Without C and activation the blocks are unrolled, over two LDS buffers where
 // they fit, block i + 1 written before block i is read: with one wave on each SIMD

@@ -4,7 +4,8 @@
 // Bound by memory (a row is read once and held in registers between the
 // maximum and the rounding), so the arithmetic for each value is kept to six
 // instructions for 16-bit inputs.  Rows of bf16: 4096 x 16384 in 45 us (4.4 TB/s),
-// 2048 x 4096 in 8.2, up to 256 rows of up to 8192 in 3 to 4 (a launch).
+// 2048 x 4096 in 8.2, up to 256 rows of up to 8192 in 3 to 4 (a launch); of fp32: 4096
+// x 16384 in 67 (5.0 TB/s), 2048 x 4096 in 9.4, 64 x 16384 in 5.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -399,9 +399,13 @@ int gemm_validate_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx
  * Speed: vector loads as for gemm_run.  With K-contiguous operands (row-major A,
  * column-major B) and vector loads, up to 32 rows stream B from memory once, a
  * column block for each workgroup, and calls of few output tiles take deeply
- * pipelined ones; other calls run the int8 tiles.  Operands that miss the
+ * pipelined ones; other calls run the int8 tiles.  Nothing splits K between
+ * workgroups, so few rows with a row-major B leave most of the GPU idle (1 to 128 x
+ * 4096 x 16384: 102 us, with a column-major B 14 to 30).  Operands that miss the
  * vector loads are read element by element (gemm_run copies large ones into its
- * workspace first; this call has none).
+ * workspace first; this call has none): lines of 16392 instead of 16384 bytes take 1
+ * x 4096 x 16384 from 14 to 684 us.  C is read element by element too (4096^3 in bf16:
+ * 74 us, 117 with C).
  */
 int gemm_run_scaled(int64_t M, int64_t N, int64_t K,
                     const void *A, int64_t lda, int layoutA,
@@ -473,8 +477,10 @@ int gemm_validate_scaled(int64_t M, int64_t N, int64_t K,
  * applied to the fp32 sums.  An Inf in a chosen expert's W2 gives NaN.
  *
  * Speed: bound by the chosen experts' weights, each read once.  16-byte loads
- * where X, W1 and W2 are 16-byte aligned with lines of whole 16 bytes; element
- * by element otherwise (slow).
+ * where X, W1 and W2 are all 16-byte aligned with lines of whole 16 bytes; element
+ * by element, all three, otherwise (slow).  With more than 256 experts and fewer than
+ * that many pairs of token and expert the routing outweighs them (8 tokens, top 8 of
+ * int8 experts of 512 x 256: 48 us with 256 experts, 190 with 512, 1204 with 1024).
  *
  * Errors: GEMM_ERR_INVALID_DIM (T < 0; H, I, E or topk out of range above or
  * topk > E), GEMM_ERR_UNSUPPORTED (T > 64, E > 1024, topk > 32, a dtype or
