@@ -30,6 +30,13 @@ __all__ = [
     "gemm_quantize_rows", "gemm_validate_quantize_rows",
     "gemm_run_scaled", "gemm_validate_scaled",
     "GEMM_ACT_SILU", "GemmMoe", "gemm_moe_run", "gemm_moe_workspace", "gemm_validate_moe",
+    "gemm_moe_balance", "gemm_moe_balance_grad", "gemm_moe_balance_workspace",
+    "gemm_validate_moe_balance", "gemm_validate_moe_balance_grad",
+    "GemmLora", "gemm_lora_run", "gemm_lora_workspace", "gemm_validate_lora",
+    "gemm_checkpoint_pack", "gemm_checkpoint_unpack", "gemm_checkpoint_act_grad",
+    "gemm_checkpoint_wgrad", "gemm_checkpoint_wgrad_workspace", "gemm_validate_checkpoint_pack",
+    "gemm_validate_checkpoint_unpack", "gemm_validate_checkpoint_act_grad",
+    "gemm_validate_checkpoint_wgrad",
     "gemm_autotune", "gemm_autotune_lookup", "gemm_autotune_clear",
 ]
 
@@ -77,8 +84,24 @@ class GemmMoe(ctypes.Structure):
                          scale2 or None, w_dtype, activation, int(renormalize))
 
 
+class GemmLora(ctypes.Structure):
+    """gemm_lora_t: the low-rank adapters of one projection.
+
+    ``A``, ``B``, ``ranks`` and ``scales`` are device addresses (int); the last two may
+    be 0 for none."""
+    _fields_ = [("K", ctypes.c_int64), ("N", ctypes.c_int64), ("adapters", ctypes.c_int64),
+                ("rank", ctypes.c_int64), ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("ranks", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+    def __init__(self, K, N, adapters, rank, A, lda, B, ldb, ranks=0, scales=0):
+        super().__init__(K, N, adapters, rank, A or None, lda, B or None, ldb, ranks or None,
+                         scales or None)
+
+
 # Exported symbols and their C signatures (mirrors include/libgemm.h).
 _i64, _int, _vp, _cp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_char_p
+_f32 = ctypes.c_float
 _GEMM_ARGS = [_i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _i64,
               _int, _int, _int, _int, _vp]
 SIGNATURES = {
@@ -106,6 +129,33 @@ SIGNATURES = {
     "gemm_moe_workspace": (_i64, [_i64, ctypes.POINTER(GemmMoe)]),
     "gemm_validate_moe": (_int, [_i64, ctypes.POINTER(GemmMoe), _vp, _i64, _vp, _i64, _vp, _i64,
                                  _int, _vp, _i64]),
+    "gemm_moe_balance": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _f32, _f32, _vp, _vp, _vp, _vp,
+                                _i64, _vp]),
+    "gemm_moe_balance_grad": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _f32, _f32, _vp, _vp, _vp,
+                                     _vp, _i64, _int, _vp]),
+    "gemm_moe_balance_workspace": (_i64, [_i64, _i64, _i64]),
+    "gemm_validate_moe_balance": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _f32, _f32, _vp, _vp,
+                                         _vp, _vp, _i64]),
+    "gemm_validate_moe_balance_grad": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _f32, _f32, _vp,
+                                              _vp, _vp, _vp, _i64, _int]),
+    "gemm_lora_run": (_int, [_i64, ctypes.POINTER(GemmLora), _vp, _i64, _vp, _vp, _i64, _vp, _i64,
+                             _int, _int, _vp, _i64, _vp]),
+    "gemm_lora_workspace": (_i64, [_i64, ctypes.POINTER(GemmLora)]),
+    "gemm_validate_lora": (_int, [_i64, ctypes.POINTER(GemmLora), _vp, _i64, _vp, _vp, _i64, _vp,
+                                  _i64, _int, _int, _vp, _i64]),
+    "gemm_checkpoint_pack": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp]),
+    "gemm_checkpoint_unpack": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp]),
+    "gemm_checkpoint_act_grad": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp,
+                                        _i64, _int, _vp]),
+    "gemm_checkpoint_wgrad": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                     _vp, _i64, _int, _int, _vp, _i64, _vp]),
+    "gemm_checkpoint_wgrad_workspace": (_i64, [_i64, _i64, _i64]),
+    "gemm_validate_checkpoint_pack": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64]),
+    "gemm_validate_checkpoint_unpack": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int]),
+    "gemm_validate_checkpoint_act_grad": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int,
+                                                 _vp, _i64, _int]),
+    "gemm_validate_checkpoint_wgrad": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                              _vp, _i64, _vp, _i64, _int, _int, _vp, _i64]),
     "gemm_autotune": (_int, _GEMM_ARGS[:-1] + [ctypes.POINTER(GemmEpilogue), _int,
                                               ctypes.POINTER(_int), _vp]),
     "gemm_autotune_lookup": (_int, [_i64, _i64, _i64, _int, _int, _int, _int, _int, _int]),
@@ -271,6 +321,130 @@ def gemm_validate_moe(T, layer, X, ldx, logits, ldl, D, ldd, in_dtype, workspace
     return library().gemm_validate_moe(T, _epi_ref(layer), X or None, ldx, logits or None, ldl,
                                        D or None, ldd, in_dtype, workspace or None,
                                        workspace_bytes)
+
+
+def gemm_moe_balance(T, E, topk, logits, ldl, mask, balance, z, loss, counts, lse, workspace,
+                     workspace_bytes, stream) -> int:
+    """Enqueue the router's balance loss, its per-expert counts and the rows' log-sum-exps;
+    returns the status code."""
+    return library().gemm_moe_balance(T, E, topk, logits or None, ldl, mask or None, balance, z,
+                                      loss or None, counts or None, lse or None,
+                                      workspace or None, workspace_bytes, stream or None)
+
+
+def gemm_moe_balance_grad(T, E, topk, logits, ldl, mask, balance, z, counts, lse, dloss, D, ldd,
+                          out_dtype, stream) -> int:
+    """Enqueue the gradient of gemm_moe_balance's loss with respect to the logits; returns
+    the status code."""
+    return library().gemm_moe_balance_grad(T, E, topk, logits or None, ldl, mask or None, balance,
+                                           z, counts or None, lse or None, dloss or None,
+                                           D or None, ldd, out_dtype, stream or None)
+
+
+def gemm_moe_balance_workspace(T, E, topk) -> int:
+    """Bytes of device workspace that gemm_moe_balance needs, or a negative status code."""
+    return library().gemm_moe_balance_workspace(T, E, topk)
+
+
+def gemm_validate_moe_balance(T, E, topk, logits, ldl, mask, balance, z, loss, counts, lse,
+                              workspace, workspace_bytes) -> int:
+    """Host-only argument check of gemm_moe_balance; returns the status code."""
+    return library().gemm_validate_moe_balance(T, E, topk, logits or None, ldl, mask or None,
+                                               balance, z, loss or None, counts or None,
+                                               lse or None, workspace or None, workspace_bytes)
+
+
+def gemm_validate_moe_balance_grad(T, E, topk, logits, ldl, mask, balance, z, counts, lse, dloss,
+                                   D, ldd, out_dtype) -> int:
+    """Host-only argument check of gemm_moe_balance_grad; returns the status code."""
+    return library().gemm_validate_moe_balance_grad(T, E, topk, logits or None, ldl, mask or None,
+                                                    balance, z, counts or None, lse or None,
+                                                    dloss or None, D or None, ldd, out_dtype)
+
+
+def gemm_lora_run(T, lora, X, ldx, ids, C, ldc, D, ldd, in_dtype, out_dtype, workspace,
+                  workspace_bytes, stream) -> int:
+    """Enqueue D = C + the low-rank adapters ``lora`` (a GemmLora), one for each of T
+    tokens by ``ids``; returns the status code."""
+    return library().gemm_lora_run(T, _epi_ref(lora), X or None, ldx, ids or None, C or None, ldc,
+                                   D or None, ldd, in_dtype, out_dtype, workspace or None,
+                                   workspace_bytes, stream or None)
+
+
+def gemm_lora_workspace(T, lora) -> int:
+    """Bytes of device workspace that gemm_lora_run needs, or a negative status code."""
+    return library().gemm_lora_workspace(T, _epi_ref(lora))
+
+
+def gemm_validate_lora(T, lora, X, ldx, ids, C, ldc, D, ldd, in_dtype, out_dtype, workspace,
+                       workspace_bytes) -> int:
+    """Host-only argument check of gemm_lora_run; returns the status code."""
+    return library().gemm_validate_lora(T, _epi_ref(lora), X or None, ldx, ids or None, C or None,
+                                        ldc, D or None, ldd, in_dtype, out_dtype,
+                                        workspace or None, workspace_bytes)
+
+
+def gemm_checkpoint_pack(M, K, X, ldx, in_dtype, Q, ldq, S, lds, stream) -> int:
+    """Enqueue the packing of X to int8 ``Q`` with a power of two ``S`` for each 32 values
+    of a row; returns the status code."""
+    return library().gemm_checkpoint_pack(M, K, X or None, ldx, in_dtype, Q or None, ldq,
+                                          S or None, lds, stream or None)
+
+
+def gemm_checkpoint_unpack(M, K, Q, ldq, S, lds, D, ldd, out_dtype, stream) -> int:
+    """Enqueue D = the values that Q and S stand for; returns the status code."""
+    return library().gemm_checkpoint_unpack(M, K, Q or None, ldq, S or None, lds, D or None, ldd,
+                                            out_dtype, stream or None)
+
+
+def gemm_checkpoint_act_grad(M, K, Q, ldq, S, lds, G, ldg, activation, D, ldd, dtype,
+                             stream) -> int:
+    """Enqueue D = G * act'(the values that Q and S stand for); returns the status code."""
+    return library().gemm_checkpoint_act_grad(M, K, Q or None, ldq, S or None, lds, G or None, ldg,
+                                              activation, D or None, ldd, dtype, stream or None)
+
+
+def gemm_checkpoint_wgrad(M, N, K, G, ldg, Q, ldq, S, lds, C, ldc, D, ldd, in_dtype, out_dtype,
+                          workspace, workspace_bytes, stream) -> int:
+    """Enqueue D = G^T x (the values that Q and S stand for) + C; returns the status code."""
+    return library().gemm_checkpoint_wgrad(M, N, K, G or None, ldg, Q or None, ldq, S or None, lds,
+                                           C or None, ldc, D or None, ldd, in_dtype, out_dtype,
+                                           workspace or None, workspace_bytes, stream or None)
+
+
+def gemm_checkpoint_wgrad_workspace(M, N, K) -> int:
+    """Bytes of device workspace that gemm_checkpoint_wgrad needs (possibly 0), or a
+    negative status code."""
+    return library().gemm_checkpoint_wgrad_workspace(M, N, K)
+
+
+def gemm_validate_checkpoint_pack(M, K, X, ldx, in_dtype, Q, ldq, S, lds) -> int:
+    """Host-only argument check of gemm_checkpoint_pack; returns the status code."""
+    return library().gemm_validate_checkpoint_pack(M, K, X or None, ldx, in_dtype, Q or None, ldq,
+                                                   S or None, lds)
+
+
+def gemm_validate_checkpoint_unpack(M, K, Q, ldq, S, lds, D, ldd, out_dtype) -> int:
+    """Host-only argument check of gemm_checkpoint_unpack; returns the status code."""
+    return library().gemm_validate_checkpoint_unpack(M, K, Q or None, ldq, S or None, lds,
+                                                     D or None, ldd, out_dtype)
+
+
+def gemm_validate_checkpoint_act_grad(M, K, Q, ldq, S, lds, G, ldg, activation, D, ldd,
+                                      dtype) -> int:
+    """Host-only argument check of gemm_checkpoint_act_grad; returns the status code."""
+    return library().gemm_validate_checkpoint_act_grad(M, K, Q or None, ldq, S or None, lds,
+                                                       G or None, ldg, activation, D or None, ldd,
+                                                       dtype)
+
+
+def gemm_validate_checkpoint_wgrad(M, N, K, G, ldg, Q, ldq, S, lds, C, ldc, D, ldd, in_dtype,
+                                   out_dtype, workspace, workspace_bytes) -> int:
+    """Host-only argument check of gemm_checkpoint_wgrad; returns the status code."""
+    return library().gemm_validate_checkpoint_wgrad(M, N, K, G or None, ldg, Q or None, ldq,
+                                                    S or None, lds, C or None, ldc, D or None, ldd,
+                                                    in_dtype, out_dtype, workspace or None,
+                                                    workspace_bytes)
 
 
 def gemm_autotune(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd,

@@ -224,4 +224,252 @@ inline int validate_moe(int64_t T, const gemm_moe_t *m, const void *X, int64_t l
     return GEMM_OK;
 }
 
+// The router's balance: dimensions, then what both directions read.
+inline int validate_moe_balance_dims(int64_t T, int64_t E, int64_t topk) {
+    if (T < 0 || T > 0x7fffffff || E < 1 || topk < 1 || topk > E) return GEMM_ERR_INVALID_DIM;
+    if (E > 1024 || topk > 32) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+inline bool finite_weight(float w) { return w - w == 0.0f; }
+
+// Parts of the workspace, from its start rounded up to 256 bytes: for each of up to
+// kBalanceParts workgroups the sums of p and the counts of its tokens, by expert.
+constexpr int64_t kBalanceParts = 256;
+inline int64_t moe_balance_workspace(int64_t E) { return kBalanceParts * (E + 1) * 12 + 255; }
+
+inline int validate_moe_balance(int64_t T, int64_t E, int64_t topk, const float *logits,
+                                int64_t ldl, const uint8_t *mask, float balance, float z,
+                                const float *loss, const int32_t *counts, const float *lse,
+                                const void *workspace, int64_t workspace_bytes) {
+    const int st = validate_moe_balance_dims(T, E, topk);
+    if (st != GEMM_OK) return st;
+    if (!finite_weight(balance) || !finite_weight(z)) return GEMM_ERR_UNSUPPORTED;
+    const int64_t kMaxLd = (int64_t)1 << 40;
+    if (ldl < E || ldl > kMaxLd) return GEMM_ERR_INVALID_LD;
+    if (!loss || !counts || !workspace || (T > 0 && (!logits || !lse))) return GEMM_ERR_NULL_PTR;
+    const int64_t need = moe_balance_workspace(E);
+    if (workspace_bytes < need) return GEMM_ERR_SCRATCH_TOO_SMALL;
+    const Range in[2] = {extent(logits, T, E, ldl, 4), extent(mask, mask ? 1 : 0, T, T, 1)};
+    const Range out[4] = {extent(loss, 1, 3, 3, 4), extent(counts, 1, E + 1, E + 1, 4),
+                          extent(lse, 1, T, T, 4), extent(workspace, 1, need, need, 1)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range &r : in)
+            if (overlap(r, out[i])) return GEMM_ERR_ALIASING;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return GEMM_ERR_ALIASING;
+    }
+    return GEMM_OK;
+}
+
+inline int validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const float *logits,
+                                     int64_t ldl, const uint8_t *mask, float balance, float z,
+                                     const int32_t *counts, const float *lse, const float *dloss,
+                                     const void *D, int64_t ldd, int out_dtype) {
+    const int st = validate_moe_balance_dims(T, E, topk);
+    if (st != GEMM_OK) return st;
+    if (!finite_weight(balance) || !finite_weight(z)) return GEMM_ERR_UNSUPPORTED;
+    if (out_dtype != GEMM_F32 && out_dtype != GEMM_F16 && out_dtype != GEMM_BF16)
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t kMaxLd = (int64_t)1 << 40;
+    if (ldl < E || ldl > kMaxLd || ldd < E || ldd > kMaxLd) return GEMM_ERR_INVALID_LD;
+    if (T == 0) return GEMM_OK;
+    if (!logits || !counts || !lse || !D) return GEMM_ERR_NULL_PTR;
+    const Range rd = extent(D, T, E, ldd, out_size(out_dtype));
+    const Range in[5] = {extent(logits, T, E, ldl, 4), extent(mask, mask ? 1 : 0, T, T, 1),
+                         extent(counts, 1, E + 1, E + 1, 4), extent(lse, 1, T, T, 4),
+                         extent(dloss, dloss ? 1 : 0, 1, 1, 4)};
+    for (const Range &r : in)
+        if (overlap(r, rd)) return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
+// Low-rank adapters: the dimensions, and the workspace they need (partial sums of
+// x A^T: splits x T x rank rounded up to 8, fp32).
+inline int validate_lora_dims(int64_t T, const gemm_lora_t *l) {
+    if (!l) return GEMM_ERR_NULL_PTR;
+    const int64_t kMaxWidth = (int64_t)1 << 19, kMaxTokens = (int64_t)1 << 20;
+    if (T < 0 || l->K < 1 || l->N < 1 || l->K > kMaxWidth || l->N > kMaxWidth ||
+        l->adapters < 1 || l->rank < 1)
+        return GEMM_ERR_INVALID_DIM;
+    if (T > kMaxTokens || l->adapters > kMaxTokens || l->rank > 256) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+// Parts of K that different workgroups take: with few tiles of 16 tokens there are
+// CUs to spare, and an adapter's rows of A are long.
+inline int64_t lora_splits(int64_t T, int64_t K) {
+    const int64_t tiles = (T + 15) / 16, most = (K + 511) / 512;
+    int64_t s = 1;
+    while (s < 8 && tiles * s < 128 && 2 * s <= most) s *= 2;
+    return s;
+}
+inline int64_t lora_ldh(int64_t rank) { return (rank + 7) / 8 * 8; }
+inline int64_t lora_workspace(int64_t T, const gemm_lora_t *l) {
+    return lora_splits(T, l->K) * T * lora_ldh(l->rank) * 4 + 255;
+}
+
+inline int validate_lora(int64_t T, const gemm_lora_t *l, const void *X, int64_t ldx,
+                         const int32_t *ids, const void *C, int64_t ldc, const void *D,
+                         int64_t ldd, int in_dtype, int out_dtype, const void *workspace,
+                         int64_t workspace_bytes) {
+    const int st = validate_lora_dims(T, l);
+    if (st != GEMM_OK) return st;
+    if (in_dtype != GEMM_F16 && in_dtype != GEMM_BF16) return GEMM_ERR_UNSUPPORTED;
+    if (out_dtype != GEMM_F32 && out_dtype != GEMM_F16 && out_dtype != GEMM_BF16)
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t kMaxLd = (int64_t)1 << 24;
+    auto ld_bad = [&](int64_t ld, int64_t inner) { return ld < inner || ld > kMaxLd; };
+    if (ld_bad(ldx, l->K) || ld_bad(l->lda, l->K) || ld_bad(l->ldb, l->rank) || ld_bad(ldd, l->N) ||
+        (C && ld_bad(ldc, l->N)))
+        return GEMM_ERR_INVALID_LD;
+    if (T == 0) return GEMM_OK;
+    if (!X || !ids || !D || !workspace || !l->A || !l->B) return GEMM_ERR_NULL_PTR;
+    const int64_t need = lora_workspace(T, l);
+    if (workspace_bytes < need) return GEMM_ERR_SCRATCH_TOO_SMALL;
+    const int osz = out_size(out_dtype);
+    const int64_t n = l->adapters;
+    const Range rd = extent(D, T, l->N, ldd, osz), rw = extent(workspace, 1, need, need, 1);
+    const Range in[6] = {extent(X, T, l->K, ldx, 2),
+                         extent(ids, 1, T, T, 4),
+                         extent(l->A, n * l->rank, l->K, l->lda, 2),
+                         extent(l->B, n * l->N, l->rank, l->ldb, 2),
+                         extent(l->ranks, l->ranks ? 1 : 0, n, n, 4),
+                         extent(l->scales, l->scales ? 1 : 0, n, n, 4)};
+    if (overlap(rd, rw)) return GEMM_ERR_ALIASING;
+    for (const Range &r : in)
+        if (overlap(r, rd) || overlap(r, rw)) return GEMM_ERR_ALIASING;
+    if (C) {
+        const Range rc = extent(C, T, l->N, ldc, osz);
+        if (overlap(rc, rw) || (!(C == D && ldc == ldd) && overlap(rc, rd)))
+            return GEMM_ERR_ALIASING;
+    }
+    return GEMM_OK;
+}
+
+// Activation checkpoints: M x K values in blocks of 32 along K.
+constexpr int64_t kCheckpointBlock = 32;
+inline int64_t checkpoint_blocks(int64_t K) {
+    return (K + kCheckpointBlock - 1) / kCheckpointBlock;
+}
+inline bool is_float(int dt) { return dt == GEMM_F32 || dt == GEMM_F16 || dt == GEMM_BF16; }
+
+inline int validate_checkpoint_dims(int64_t M, int64_t K, int64_t ldq, int64_t lds) {
+    const int64_t kMaxDim = 0x7fffffff, kMaxLd = (int64_t)1 << 40;
+    if (M < 0 || K < 0 || M > kMaxDim || K > kMaxDim) return GEMM_ERR_INVALID_DIM;
+    if (ldq < 1 || ldq < K || ldq > kMaxLd) return GEMM_ERR_INVALID_LD;
+    if (lds < 1 || lds < checkpoint_blocks(K) || lds > kMaxLd) return GEMM_ERR_INVALID_LD;
+    return GEMM_OK;
+}
+inline bool line_bad(int64_t ld, int64_t inner) {
+    return ld < 1 || ld < inner || ld > ((int64_t)1 << 40);
+}
+
+inline int validate_checkpoint_pack(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype,
+                                    const void *Q, int64_t ldq, const uint8_t *S, int64_t lds) {
+    const int st = validate_checkpoint_dims(M, K, ldq, lds);
+    if (st != GEMM_OK) return st;
+    if (!is_float(in_dtype)) return GEMM_ERR_UNSUPPORTED;
+    if (line_bad(ldx, K)) return GEMM_ERR_INVALID_LD;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!X || !Q || !S) return GEMM_ERR_NULL_PTR;
+    const Range rx = extent(X, M, K, ldx, out_size(in_dtype)), rq = extent(Q, M, K, ldq, 1);
+    const Range rs = extent(S, M, checkpoint_blocks(K), lds, 1);
+    if (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs)) return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
+inline int validate_checkpoint_unpack(int64_t M, int64_t K, const void *Q, int64_t ldq,
+                                      const uint8_t *S, int64_t lds, const void *D, int64_t ldd,
+                                      int out_dtype) {
+    const int st = validate_checkpoint_dims(M, K, ldq, lds);
+    if (st != GEMM_OK) return st;
+    if (!is_float(out_dtype)) return GEMM_ERR_UNSUPPORTED;
+    if (line_bad(ldd, K)) return GEMM_ERR_INVALID_LD;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!Q || !S || !D) return GEMM_ERR_NULL_PTR;
+    const Range rd = extent(D, M, K, ldd, out_size(out_dtype));
+    if (overlap(rd, extent(Q, M, K, ldq, 1)) ||
+        overlap(rd, extent(S, M, checkpoint_blocks(K), lds, 1)))
+        return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
+inline int validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int64_t ldq,
+                                        const uint8_t *S, int64_t lds, const void *G, int64_t ldg,
+                                        int activation, const void *D, int64_t ldd, int dtype) {
+    if (activation != GEMM_ACT_RELU && activation != GEMM_ACT_GELU && activation != GEMM_ACT_SILU)
+        return GEMM_ERR_UNSUPPORTED;
+    const int st = validate_checkpoint_unpack(M, K, Q, ldq, S, lds, D, ldd, dtype);
+    if (st != GEMM_OK) return st;
+    if (line_bad(ldg, K)) return GEMM_ERR_INVALID_LD;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!G) return GEMM_ERR_NULL_PTR;
+    const int sz = out_size(dtype);
+    if (!(G == D && ldg == ldd) && overlap(extent(G, M, K, ldg, sz), extent(D, M, K, ldd, sz)))
+        return GEMM_ERR_ALIASING;
+    return GEMM_OK;
+}
+
+// The weight gradient's tiles and the parts of its tokens that different workgroups
+// take, from the sizes alone (for the 256 CUs of a whole device), so that the workspace
+// a program reserves fits whatever the device.
+struct WgradPlan {
+    int64_t bm, bn, splits, per;  // per: tokens of a part, a multiple of 64
+};
+inline WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
+    WgradPlan w;
+    w.bm = N <= 32 ? 32 : 128;
+    w.bn = 128;
+    const int64_t tiles = ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
+    const int64_t steps = (M + 63) / 64;
+    // parts of at least 4 steps while fewer than two workgroups for each CU are left
+    int64_t s = tiles > 0 ? 512 / tiles : 1;
+    if (s > steps / 4) s = steps / 4;
+    if (s > 64) s = 64;
+    if (s < 1) s = 1;
+    w.per = steps > 0 ? (steps + s - 1) / s * 64 : 64;
+    w.splits = steps > 0 ? (steps * 64 + w.per - 1) / w.per : 1;
+    return w;
+}
+
+inline int64_t checkpoint_wgrad_workspace(int64_t M, int64_t N, int64_t K) {
+    const int64_t kMaxDim = 0x7fffffff;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return GEMM_ERR_INVALID_DIM;
+    if (M == 0 || N == 0 || K == 0) return 0;
+    const WgradPlan w = wgrad_plan(M, N, K);
+    return w.splits > 1 ? w.splits * N * K * 4 + 255 : 0;
+}
+
+inline int validate_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_t ldg,
+                                     const void *Q, int64_t ldq, const uint8_t *S, int64_t lds,
+                                     const void *C, int64_t ldc, const void *D, int64_t ldd,
+                                     int in_dtype, int out_dtype, const void *workspace,
+                                     int64_t workspace_bytes) {
+    const int64_t need = checkpoint_wgrad_workspace(M, N, K);
+    if (need < 0) return (int)need;
+    const int st = validate_checkpoint_dims(M, K, ldq, lds);
+    if (st != GEMM_OK) return st;
+    if ((in_dtype != GEMM_F16 && in_dtype != GEMM_BF16) || !is_float(out_dtype))
+        return GEMM_ERR_UNSUPPORTED;
+    if (line_bad(ldg, N) || line_bad(ldd, K) || (C && line_bad(ldc, K))) return GEMM_ERR_INVALID_LD;
+    if (N == 0 || K == 0) return GEMM_OK;
+    if (!D || (M > 0 && (!G || !Q || !S)) || (need > 0 && !workspace)) return GEMM_ERR_NULL_PTR;
+    if (workspace_bytes < need) return GEMM_ERR_SCRATCH_TOO_SMALL;
+    const int osz = out_size(out_dtype);
+    const Range rd = extent(D, N, K, ldd, osz), rw = extent(workspace, need > 0 ? 1 : 0, need, need, 1);
+    const Range in[3] = {extent(G, M, N, ldg, 2), extent(Q, M, K, ldq, 1),
+                         extent(S, M, checkpoint_blocks(K), lds, 1)};
+    if (overlap(rd, rw)) return GEMM_ERR_ALIASING;
+    for (const Range &r : in)
+        if (overlap(r, rd) || overlap(r, rw)) return GEMM_ERR_ALIASING;
+    if (C) {
+        const Range rc = extent(C, N, K, ldc, osz);
+        if (overlap(rc, rw) || (!(C == D && ldc == ldd) && overlap(rc, rd)))
+            return GEMM_ERR_ALIASING;
+    }
+    return GEMM_OK;
+}
+
 }  // namespace libgemm_host

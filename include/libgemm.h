@@ -84,7 +84,8 @@ typedef enum {
                                      config cannot run this problem            */
     GEMM_ERR_SCRATCH_TOO_SMALL = -9 /* gemm_run_noalloc: the split-K partial
                                      sums need more than its fixed scratch;
-                                     gemm_moe_run: workspace_bytes too small   */
+                                     a call with a workspace of the caller's:
+                                     workspace_bytes too small                */
 } gemm_status_t;
 
 /*
@@ -276,7 +277,7 @@ typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1,
     GEMM_ACT_GELU = 2,
-    GEMM_ACT_SILU = 3  /* x / (1 + exp(-x)); gemm_moe_run only */
+    GEMM_ACT_SILU = 3  /* x / (1 + exp(-x)); gemm_moe_run, gemm_checkpoint_act_grad only */
 } gemm_activation_t;
 
 typedef struct {
@@ -513,6 +514,245 @@ int64_t gemm_moe_workspace(int64_t T, const gemm_moe_t *layer);
 int gemm_validate_moe(int64_t T, const gemm_moe_t *layer, const void *X, int64_t ldx,
                       const float *logits, int64_t ldl, const void *D, int64_t ldd, int in_dtype,
                       const void *workspace, int64_t workspace_bytes);
+
+/* ============================================ balance of a router's experts
+ *
+ * The loss that keeps a trained router from using a few experts only, the tokens
+ * of each expert, and the loss's gradient.  For T tokens with logits l (T x E),
+ * the choice of experts being gemm_moe_run's (the topk largest logits, ties to
+ * the lower index, none at -Inf or NaN), over the n tokens that count:
+ *
+ *   p_te = exp(l_te - lse_t),   lse_t = log sum_e exp(l_te)
+ *   c_e  = tokens that chose e,   f_e = c_e / (n topk),   P_e = sum_t p_te / n
+ *   loss[1] = E sum_e f_e P_e       (1 when all experts are used alike)
+ *   loss[2] = sum_t lse_t^2 / n     (keeps the logits from drifting)
+ *   loss[0] = balance * loss[1] + z * loss[2]
+ *
+ * and, with f held constant (a count has no slope) and g = *dloss (1 if NULL),
+ *
+ *   D_te = g / n * ( balance E p_te (f_e - sum_j f_j p_tj) + 2 z lse_t p_te ).
+ *
+ * A token does not count where mask is given and mask[t] is 0, or where all of its
+ * logits are -Inf: it adds nothing, and its row of D is 0.  With n == 0 the loss and
+ * D are 0.  A counted token with a NaN or +Inf among its logits makes the loss and its
+ * own row of D NaN, and no other row.
+ *
+ *   T            tokens, 0 to 2^31-1
+ *   E, topk      1 to 1024 experts, 1 to 32 of them (<= E) for a token
+ *   logits, ldl  fp32, row-major, ldl >= E
+ *   mask         T bytes on the device, or NULL (every token counts).  A token that
+ *                does not count is not read.
+ *   loss         3 fp32 values (gemm_moe_balance writes)
+ *   counts       E + 1 int32: c_e, then n (gemm_moe_balance writes, _grad reads)
+ *   lse          T fp32 values; 0 for a masked token, -Inf for one whose logits all are
+ *                (gemm_moe_balance writes, _grad reads)
+ *   dloss        one fp32 value on the device, the gradient of loss[0], or NULL (1)
+ *   D, ldd       T x E of out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16), row-major; nothing
+ *                outside is written
+ *   workspace    device memory of at least gemm_moe_balance_workspace(T, E, topk) bytes,
+ *                of any content, owned by the caller, written by the call.  Calls that
+ *                may overlap need workspaces of their own.
+ * gemm_moe_balance enqueues two kernels, gemm_moe_balance_grad one.  Both allocate
+ * nothing, can be captured into a HIP graph, and give the same bits for the same call.
+ *
+ * Accuracy: softmax and logarithm are fp32 (a p below 2^-126 may be 0); sums over tokens
+ * are fp64; D is rounded once.
+ *
+ * Errors: GEMM_ERR_INVALID_DIM (T < 0 or above 2^31-1, E or topk < 1, topk > E),
+ * GEMM_ERR_UNSUPPORTED (E > 1024, topk > 32, out_dtype; a weight that is not finite),
+ * GEMM_ERR_INVALID_LD, GEMM_ERR_NULL_PTR, GEMM_ERR_ALIASING (what is written overlapping
+ * another argument), GEMM_ERR_SCRATCH_TOO_SMALL, GEMM_ERR_HIP.
+ */
+int gemm_moe_balance(int64_t T, int64_t E, int64_t topk, const float *logits, int64_t ldl,
+                     const uint8_t *mask, float balance, float z, float *loss, int32_t *counts,
+                     float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+int gemm_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const float *logits, int64_t ldl,
+                          const uint8_t *mask, float balance, float z, const int32_t *counts,
+                          const float *lse, const float *dloss, void *D, int64_t ldd,
+                          int out_dtype, void *stream);
+
+/* Bytes of workspace, or a negative gemm_status_t. */
+int64_t gemm_moe_balance_workspace(int64_t T, int64_t E, int64_t topk);
+
+/* Host-only argument checks (see gemm_validate). */
+int gemm_validate_moe_balance(int64_t T, int64_t E, int64_t topk, const float *logits, int64_t ldl,
+                              const uint8_t *mask, float balance, float z, const float *loss,
+                              const int32_t *counts, const float *lse, const void *workspace,
+                              int64_t workspace_bytes);
+int gemm_validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const float *logits,
+                                   int64_t ldl, const uint8_t *mask, float balance, float z,
+                                   const int32_t *counts, const float *lse, const float *dloss,
+                                   const void *D, int64_t ldd, int out_dtype);
+
+/* ===================================================== low-rank adapters
+ *
+ * Adapters of many requests at once beside a shared projection.  For each token t
+ * with a = ids[t],
+ *
+ *   D(t,:) = C(t,:) + s_a * (x_t A_a^T) B_a^T,
+ *
+ * and D(t,:) = C(t,:) where ids[t] names no adapter (any value outside [0, adapters)).
+ * C is the shared projection's output (e.g. gemm_run's or gemm_run_scaled's D).
+ *
+ * gemm_lora_t describes the adapters of one projection:
+ *   K, N         input and output width, 1 to 2^19
+ *   adapters     1 to 2^20
+ *   rank         rows kept for each adapter, 1 to 256
+ *   A, lda       adapters x rank rows of K elements, lines lda >= K elements apart
+ *   B, ldb       adapters x N rows of rank elements, lines ldb >= rank elements apart
+ *   ranks        device pointer to one int32 for each adapter, its own rank (0 to rank;
+ *                what lies outside is clamped), or NULL (rank for all).  Rows of A and
+ *                columns of B from the adapter's rank on are not part of it.
+ *   scales       device pointer to one fp32 for each adapter, or NULL (1)
+ *
+ * gemm_lora_run:
+ *   T            tokens, 0 to 2^20
+ *   X, ldx       T x K of in_dtype (GEMM_F16 or GEMM_BF16, the type of A and B too)
+ *   ids          T int32 on the device, in any order
+ *   C, ldc       T x N of out_dtype, row-major, or NULL (C = 0).  C == D with ldc == ldd is
+ *                the in-place update; any other overlap is refused.
+ *   D, ldd       T x N of out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16), row-major; nothing
+ *                outside is written
+ *   workspace    device memory of at least gemm_lora_workspace(T, lora) bytes, of any
+ *                content, owned by the caller, written by the call.  A call must not overlap
+ *                another one (or a graph's replay) that uses the same workspace, unless the
+ *                caller orders them.
+ * The call enqueues two kernels and allocates nothing, so it can be captured into a HIP
+ * graph; which tokens use which adapter is found on the device, and a replay follows the
+ * ids of its own time.  Tokens do not touch each other: what an adapter holds (an Inf, a
+ * NaN) reaches its own tokens only.  The same call gives the same bits.
+ *
+ * Accuracy: products and sums are fp32.  The second product takes h = x A^T as a sum of
+ * values of in_dtype: two of them for a 16-bit D (16 significant bits for bf16, 22 for fp16),
+ * three for an fp32 D (24 and 33).  fp16 parts are those of h times a power of two that
+ * follows the token's largest |h|, so h may lie anywhere in fp32's range, and what is below
+ * 2^-34 (fp32 D: 2^-38) of that largest value is lost.  D is rounded once.
+ *
+ * Speed: 16-byte loads of X and A where both are 16-byte aligned with lines of whole 16
+ * bytes, of B and of C and D alike; element by element otherwise.  Tokens are taken in tiles
+ * of consecutive ones, and an adapter's weights are read once for each tile that it has
+ * tokens in: packed prompts, or few tokens, in any order; thousands of tokens whose adapters
+ * change from one to the next read the weights again for every tile.
+ *
+ * Errors: GEMM_ERR_INVALID_DIM (T < 0; K, N, adapters or rank < 1; K or N > 2^19),
+ * GEMM_ERR_UNSUPPORTED (T > 2^20, adapters > 2^20, rank > 256, a dtype not named above),
+ * GEMM_ERR_INVALID_LD (a line shorter than its row, or longer than 2^24 elements),
+ * GEMM_ERR_NULL_PTR, GEMM_ERR_ALIASING (D or the workspace overlapping another argument),
+ * GEMM_ERR_SCRATCH_TOO_SMALL, GEMM_ERR_HIP.
+ */
+typedef struct {
+    int64_t K, N, adapters, rank;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    const int32_t *ranks;
+    const float *scales;
+} gemm_lora_t;
+
+int gemm_lora_run(int64_t T, const gemm_lora_t *lora, const void *X, int64_t ldx,
+                  const int32_t *ids, const void *C, int64_t ldc, void *D, int64_t ldd,
+                  int in_dtype, int out_dtype, void *workspace, int64_t workspace_bytes,
+                  void *stream);
+
+/* Bytes of workspace for T tokens, or a negative gemm_status_t. */
+int64_t gemm_lora_workspace(int64_t T, const gemm_lora_t *lora);
+
+/* Host-only argument check of gemm_lora_run (see gemm_validate). */
+int gemm_validate_lora(int64_t T, const gemm_lora_t *lora, const void *X, int64_t ldx,
+                       const int32_t *ids, const void *C, int64_t ldc, const void *D, int64_t ldd,
+                       int in_dtype, int out_dtype, const void *workspace,
+                       int64_t workspace_bytes);
+
+/* ====================================== activation checkpoints in 8 bits
+ *
+ * Activations kept for the backward pass in 8 bits and a quarter, and what the
+ * backward pass does with them.  The format is MXINT8 of the OCP Microscaling
+ * Formats specification (version 1.0): 32 consecutive values of a row (the last
+ * block of a row may be shorter) share a power of two, one byte S (E8M0), and each
+ * value is an int8 Q:
+ *
+ *   X^(m,k) = 2^(S(m, k/32) - 127) * Q(m,k) / 64.
+ *
+ * X^ has at most seven significant bits and a power of two, so it is exact in bf16
+ * (and in fp16 where X was fp16), and the matrix units multiply it as it is: the
+ * rounding of gemm_checkpoint_pack is the only one.
+ *   Q, ldq       int8, M x K, row-major, ldq >= K
+ *   S, lds       bytes, M x ceil(K / 32), row-major, lds >= ceil(K / 32)
+ * Nothing outside the matrices is written.  No call allocates; all can be captured
+ * into a HIP graph; calls on different streams do not touch each other.
+ *
+ * gemm_checkpoint_pack: for each block with a = max |X|,
+ *   S = 127 + floor(log2(a)), at least 0 (a = 0: S = 0),
+ *   Q = X * 64 / 2^(S - 127), rounded to nearest even, held in [-127, 127].
+ * |X^ - X| is at most half a step of 2^(S - 133), or less than a whole one where Q was
+ * held back (|X| within a half step of 2^(S - 126)).  A block that holds an Inf or a NaN
+ * gets S = 255 and zeros, which stand for NaN.
+ *   X, ldx       M x K of in_dtype (GEMM_F16, GEMM_BF16 or GEMM_F32), row-major
+ *
+ * gemm_checkpoint_unpack: D = X^, rounded once to out_dtype (GEMM_F32, GEMM_F16 or
+ * GEMM_BF16; exact but for fp16 values outside its range).
+ *
+ * gemm_checkpoint_act_grad: D = G * act'(X^), rounded once; G and D of `dtype`, M x K,
+ * row-major.  D == G with ldd == ldg is the in-place update.
+ *   activation   GEMM_ACT_RELU (act' = 1 for X^ > 0, else 0; G * NaN where X^ is NaN),
+ *                GEMM_ACT_GELU (Phi(x) + x phi(x)) or GEMM_ACT_SILU (s + x s (1 - s),
+ *                s = 1 / (1 + exp(-x)))
+ * Between X^ and the rounding everything is fp32: act' is within 1e-6 absolutely.
+ *
+ * gemm_checkpoint_wgrad: a linear layer's weight gradient, D = G^T X^ + C:
+ *   D(n,k) = sum_m G(m,n) X^(m,k) + C(n,k)
+ *   G, ldg       M x N of in_dtype (GEMM_F16 or GEMM_BF16), row-major: the gradient of
+ *                the layer's output
+ *   C, ldc       N x K of out_dtype, row-major, or NULL (C = 0).  C == D with ldc == ldd
+ *                adds up gradients in place; any other overlap is refused.
+ *   D, ldd       N x K of out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16), row-major
+ *   workspace    device memory of at least gemm_checkpoint_wgrad_workspace(M, N, K) bytes
+ *                (may be 0, then NULL is fine), of any content, owned by the caller,
+ *                written by the call.  Calls that may overlap need workspaces of their own.
+ * M, the tokens, is the reduction's length; with M == 0, D = C (or 0).  X^ is taken in
+ * in_dtype (exact as said above; with GEMM_F16, values past 65504 become Inf), products
+ * are exact and summed in fp32, and D is rounded once.  The same call gives the same bits.
+ *
+ * Speed: 16-byte accesses where the operands' base pointers and lines are whole 16 bytes
+ * (for wgrad G and Q, for the others X, G, D and Q); element by element otherwise.  With
+ * them, bytes of the padding next to a row's last element are read (up to 15 past the
+ * last row's), and never matter.
+ *
+ * Errors: GEMM_ERR_INVALID_DIM (a dimension negative or above 2^31-1), GEMM_ERR_INVALID_LD
+ * (a line shorter than its row, or longer than 2^40 elements), GEMM_ERR_NULL_PTR,
+ * GEMM_ERR_UNSUPPORTED (a dtype or activation not named), GEMM_ERR_ALIASING (what is
+ * written overlapping another argument), GEMM_ERR_SCRATCH_TOO_SMALL, GEMM_ERR_HIP.
+ */
+int gemm_checkpoint_pack(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype, void *Q,
+                         int64_t ldq, uint8_t *S, int64_t lds, void *stream);
+int gemm_checkpoint_unpack(int64_t M, int64_t K, const void *Q, int64_t ldq, const uint8_t *S,
+                           int64_t lds, void *D, int64_t ldd, int out_dtype, void *stream);
+int gemm_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int64_t ldq, const uint8_t *S,
+                             int64_t lds, const void *G, int64_t ldg, int activation, void *D,
+                             int64_t ldd, int dtype, void *stream);
+int gemm_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_t ldg,
+                          const void *Q, int64_t ldq, const uint8_t *S, int64_t lds,
+                          const void *C, int64_t ldc, void *D, int64_t ldd, int in_dtype,
+                          int out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace (possibly 0), or a negative gemm_status_t. */
+int64_t gemm_checkpoint_wgrad_workspace(int64_t M, int64_t N, int64_t K);
+
+/* Host-only argument checks (see gemm_validate). */
+int gemm_validate_checkpoint_pack(int64_t M, int64_t K, const void *X, int64_t ldx, int in_dtype,
+                                  const void *Q, int64_t ldq, const uint8_t *S, int64_t lds);
+int gemm_validate_checkpoint_unpack(int64_t M, int64_t K, const void *Q, int64_t ldq,
+                                    const uint8_t *S, int64_t lds, const void *D, int64_t ldd,
+                                    int out_dtype);
+int gemm_validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int64_t ldq,
+                                      const uint8_t *S, int64_t lds, const void *G, int64_t ldg,
+                                      int activation, const void *D, int64_t ldd, int dtype);
+int gemm_validate_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_t ldg,
+                                   const void *Q, int64_t ldq, const uint8_t *S, int64_t lds,
+                                   const void *C, int64_t ldc, const void *D, int64_t ldd,
+                                   int in_dtype, int out_dtype, const void *workspace,
+                                   int64_t workspace_bytes);
 
 /* ============================================================ autotuning
  *

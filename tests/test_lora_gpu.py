@@ -1,0 +1,280 @@
+"""GPU parity of the low-rank adapters with their definition in 64 bits.
+
+Tolerance, with e = 2^-24, r half a step of the input's 16-bit type (fp16 2^-11, bf16 2^-8)
+and R half a step of the output's: the first product's fp32 sums of K terms (in up to 8
+parts and 4 waves) are off by at most (K + 12) e sum|x a|; h is held in two parts for a
+16-bit D and three for an fp32 one, which leaves r^2 |h| resp. r^3 |h|, and for fp16 what
+is below 2^-34 (2^-38) of the token's largest |h|; the second sums 3 rank terms,
+(3 rank + 4) e sum|h b|; the scale's multiplication adds e.  C is added in fp32 (e of the
+result), and the result rounded once: R |d|.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import dense_mixed_precision_tiled_amd as lg
+from test_checkpoint_gpu import HALF_STEP, TINY, TORCH, Lines, ok, stream
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = lg.GEMM_F32, lg.GEMM_F16, lg.GEMM_BF16
+
+
+class Lora:
+    """One seeded call.  how: "vec" (16-byte lines), "odd" (unaligned everything)."""
+
+    def __init__(self, T, K, N, rank, adapters, i=BF16, o=BF16, how="vec", ids="random", ranks=False,
+                 scales=True, c=True, ints=False, seed=0):
+        self.__dict__.update(T=T, K=K, N=N, rank=rank, adapters=adapters, i=i, o=o)
+        g = torch.Generator().manual_seed(seed + T + 31 * K + 7 * N + rank)
+        t = TORCH[i]
+        if ints:
+            pick = lambda n, m: torch.randint(-2, 3, (n, m), generator=g).to(t)  # noqa: E731
+            self.X, self.A, self.B = pick(T, K), pick(adapters * rank, K), pick(adapters * N, rank)
+            self.scales = torch.randint(1, 3, (adapters,), generator=g).float() if scales else None
+            self.C = torch.randint(-9, 10, (T, N), generator=g).to(TORCH[o]) if c else None
+        else:
+            self.X = torch.randn(T, K, generator=g).to(t)
+            self.A = (torch.randn(adapters * rank, K, generator=g) / K ** 0.5).to(t)
+            self.B = (torch.randn(adapters * N, rank, generator=g) / rank ** 0.5).to(t)
+            self.scales = torch.rand(adapters, generator=g) + 0.5 if scales else None
+            self.C = torch.randn(T, N, generator=g).to(TORCH[o]) if c else None
+        if ids == "random":  # any adapter, and none for some
+            self.ids = torch.randint(-1, adapters, (T,), generator=g)
+        elif ids == "runs":  # packed prompts
+            cuts = torch.sort(torch.randint(0, max(T, 1), (7,), generator=g)).values
+            self.ids = (torch.searchsorted(cuts, torch.arange(T), right=True) * 5 + 3) % (adapters + 1) - 1
+        else:
+            self.ids = torch.tensor(ids)
+        self.ids = self.ids.to(torch.int32)
+        self.ranks = torch.randint(-1, rank + 2, (adapters,), generator=g).int() if ranks else None
+        up = lambda n, m: (n + m - 1) // m * m  # noqa: E731
+        odd = how == "odd"
+        line = lambda n, per: n + 3 if odd else up(n, per)  # noqa: E731
+        sh = 1 if odd else 0
+        self.dX = Lines(T, K, t, line(K, 8), sh, self.X)
+        self.dA = Lines(adapters * rank, K, t, line(K, 8), sh, self.A)
+        self.dB = Lines(adapters * N, rank, t, line(rank, 8), sh, self.B)
+        for d in (self.dX, self.dA, self.dB):  # what lies between the rows must not matter
+            pad = d.buf[d.shift:d.shift + d.rows * d.ld].view(d.rows, d.ld)[:, d.cols:]
+            pad.fill_(float("nan"))
+        self.dC = Lines(T, N, TORCH[o], line(N, 8), sh, self.C) if c else None
+        self.dD = Lines(T, N, TORCH[o], line(N, 8), sh)
+        self.dids = self.ids.cuda()
+        self.dranks = None if self.ranks is None else self.ranks.cuda()
+        self.dscales = None if self.scales is None else self.scales.cuda()
+        ptr = lambda x: 0 if x is None else x.data_ptr()  # noqa: E731
+        self.lora = lg.GemmLora(K, N, adapters, rank, self.dA.ptr, self.dA.ld, self.dB.ptr, self.dB.ld,
+                                ptr(self.dranks), ptr(self.dscales))
+        self.size = lg.gemm_lora_workspace(T, self.lora)
+        assert self.size >= 0
+        self.ws = torch.full((self.size + 64,), 255, dtype=torch.uint8, device="cuda")
+
+    def call(self, D=None, s=None):
+        D = self.dD if D is None else D
+        C = self.dC
+        ok(lg.gemm_lora_run(self.T, self.lora, self.dX.ptr, self.dX.ld, self.dids.data_ptr(),
+                            0 if C is None else C.ptr, D.ld, D.ptr, D.ld, self.i, self.o, self.ws.data_ptr(),
+                            self.size, stream() if s is None else s))
+        return self
+
+    def reference(self):
+        """(D, bound of its error) in 64 bits."""
+        T, K, N, rank = self.T, self.K, self.N, self.rank
+        e, r, R = 2.0 ** -24, HALF_STEP[self.i], HALF_STEP[self.o]
+        parts, low = (3, 2.0 ** -38) if self.o == F32 else (2, 2.0 ** -34)
+        X, A, B = (v.double().numpy() for v in (self.X, self.A, self.B))
+        A, B = A.reshape(self.adapters, rank, K), B.reshape(self.adapters, N, rank)
+        D = self.C.double().numpy().copy() if self.C is not None else np.zeros((T, N))
+        tol = np.zeros((T, N))
+        for t in range(T):
+            a = int(self.ids[t])
+            if a < 0 or a >= self.adapters:
+                continue
+            k = rank if self.ranks is None else min(max(int(self.ranks[a]), 0), rank)
+            if k == 0:
+                continue
+            s = 1.0 if self.scales is None else float(self.scales[a])
+            h = A[a, :k] @ X[t]
+            dh = (K + 12) * e * (np.abs(A[a, :k]) @ np.abs(X[t]))
+            dh = dh + r ** parts * (np.abs(h) + dh)
+            if self.i == F16:
+                dh = dh + low * np.abs(h).max()
+            Bk = np.abs(B[a, :, :k])
+            D[t] += s * (B[a, :, :k] @ h)
+            tol[t] = abs(s) * (Bk @ dh + (3 * rank + 6) * e * (Bk @ np.abs(h)))
+        return D, 1.01 * tol + (1.01 * R + e) * np.abs(D) + TINY[self.o]
+
+    def check(self, D=None):
+        got = (self.dD if D is None else D).get().double().numpy()
+        want, tol = self.reference()
+        assert (self.ws[self.size:] == 255).all(), "written past the workspace"
+        assert (np.abs(got - want) <= tol).all(), np.nanmax(np.abs(got - want) / tol)
+        if self.o == F32:  # by the norm: roundings of independent signs
+            assert np.linalg.norm(got - want) <= 2.0 ** -24 * (8 + self.K ** 0.5) * np.linalg.norm(want) + 1e-30
+        return got
+
+
+SHAPES = [  # T, K, N, rank, adapters
+    (1, 64, 64, 8, 3), (1, 4096, 200, 16, 5), (2, 1, 1, 1, 1), (7, 100, 33, 5, 4), (16, 256, 64, 16, 16),
+    (17, 520, 100, 12, 9), (33, 128, 300, 33, 6), (64, 1000, 70, 64, 40), (100, 96, 65, 7, 3), (5, 300, 80, 65, 2),
+    (20, 200, 48, 200, 3), (31, 130, 40, 256, 2), (300, 160, 72, 16, 7), (1000, 72, 40, 24, 5)]
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("i,o", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32), (F16, BF16)])
+@pytest.mark.parametrize("T,K,N,rank,adapters", SHAPES)
+def test_shapes(T, K, N, rank, adapters, i, o, how):
+    Lora(T, K, N, rank, adapters, i, o, how, c=(T + N) % 3 != 0, ranks=T % 2 == 0, scales=K % 3 != 0).call().check()
+
+
+@pytest.mark.parametrize("i", [BF16, F16])
+@pytest.mark.parametrize("T", [40, 257, 1100])
+def test_packed_prompts(T, i):
+    Lora(T, 264, 136, 16, 4, i, i, ids="runs").call().check()
+
+
+@pytest.mark.parametrize("i", [BF16, F16])
+@pytest.mark.parametrize("T,rank", [(3, 4), (33, 16), (300, 40)])
+def test_integers_are_exact(T, rank, i):
+    w = Lora(T, 96, 72, rank, 5, i, F32, ints=True).call()
+    assert np.array_equal(w.dD.get().double().numpy(), w.reference()[0])
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_in_place(T):
+    w = Lora(T, 128, 100, 8, 3).call()
+    first = w.dD.get()
+    w.call(w.dC)
+    assert torch.equal(w.dC.get(), first)
+
+
+def test_no_adapter_keeps_c():
+    """Ids outside [0, adapters), of any value: D is C's very bits, NaN among them."""
+    ids = [-1, 3, 2 ** 31 - 1, -2 ** 31, 0, 7, -5, 2] * 5
+    w = Lora(40, 64, 72, 8, 3, ids=ids)
+    w.C[1, 5] = float("nan")
+    w.dC.view.copy_(w.C)
+    got = w.call().dD.get()
+    none = [t for t in range(40) if not 0 <= ids[t] < 3]
+    assert torch.equal(got[none].view(torch.int16), w.C[none].view(torch.int16))
+    w.call(w.dC)
+    assert torch.equal(w.dC.get().view(torch.int16), got.view(torch.int16))
+
+
+def test_every_token_alike_and_all_different():
+    Lora(48, 136, 80, 16, 48, ids=[5] * 48).call().check()
+    Lora(48, 136, 80, 16, 48, ids=list(range(48))).call().check()
+    Lora(48, 136, 80, 16, 48, ids=[0, 1] * 24).call().check()
+    Lora(1, 136, 80, 16, 1, ids=[-1]).call().check()
+
+
+@pytest.mark.parametrize("i", [BF16, F16])
+@pytest.mark.parametrize("T", [16, 300])
+def test_bad_values_stay_with_their_tokens(T, i):
+    """NaN in an adapter's weights, Inf in a token: other tokens do not see them."""
+    w = Lora(T, 128, 96, 16, 4, i, i, ids=[t % 4 for t in range(T)])
+    clean = w.call().dD.get()
+    w.A[2 * 16 + 3, 7] = float("nan")
+    w.B[1 * 96 + 11, 4] = float("inf")
+    w.X[0, 5] = float("inf")
+    for d, v in ((w.dA, w.A), (w.dB, w.B), (w.dX, w.X)):
+        d.view.copy_(v)
+    got = w.call().dD.get()
+    for t in range(T):
+        if t % 4 == 2:
+            assert got[t].isnan().all()
+        elif t == 0:
+            assert not got[t].isfinite().any()
+        elif t % 4 == 1:
+            assert not got[t, 11].isfinite()
+            keep = [n for n in range(96) if n != 11]
+            assert torch.equal(got[t, keep], clean[t, keep])
+        else:
+            assert torch.equal(got[t], clean[t])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -30, 1.0, 2.0 ** 30, 2.0 ** 80])
+def test_fp16_inner_values_of_any_size(size):
+    """h far outside fp16's range; the scale brings the result back."""
+    w = Lora(20, 64, 40, 16, 3, F16, F32, c=False)
+    # h = x A^T carries 2^14 at most from the operands; the rest of its size through fp32
+    # partial sums is not reachable, so take it from X and A at their ends
+    f = min(max(size, 2.0 ** -18), 2.0 ** 14)
+    w.X, w.A = (w.X.float() * f ** 0.5).half(), (w.A.float() * f ** 0.5).half()
+    w.scales = w.scales / size
+    w.dX.view.copy_(w.X)
+    w.dA.view.copy_(w.A)
+    w.dscales.copy_(w.scales)
+    w.call().check()
+
+
+def test_fp16_inner_values_past_65504():
+    w = Lora(20, 512, 40, 16, 3, F16, F32, c=False)
+    w.X, w.A = torch.full_like(w.X, 200.0), torch.full_like(w.A, 30.0)  # h = 3 072 000
+    w.A[::2] = 2.0 ** -14
+    w.dX.view.copy_(w.X)
+    w.dA.view.copy_(w.A)
+    w.call().check()
+
+
+def test_inf_rank_zero_and_scale_zero():
+    w = Lora(12, 64, 40, 8, 3, ids=[0, 1, 2] * 4)
+    w.dranks = torch.tensor([0, 8, 3], dtype=torch.int32, device="cuda")
+    w.ranks = w.dranks.cpu()
+    w.lora.ranks = w.dranks.data_ptr()
+    w.scales[1] = 0.0
+    w.dscales.copy_(w.scales)
+    got = w.call().check()
+    assert np.array_equal(got[0::3], w.C[0::3].double().numpy())
+    assert np.array_equal(got[1::3], w.C[1::3].double().numpy())
+
+
+def test_two_streams_and_same_bits():
+    a, b = Lora(64, 512, 300, 16, 20), Lora(300, 256, 200, 8, 5, ids="runs", seed=3)
+    ra, rb = a.call().dD.get(), b.call().dD.get()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.call(s=s1.cuda_stream)
+        b.call(s=s2.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a.dD.get(), ra) and torch.equal(b.dD.get(), rb)
+
+
+def test_captured_follows_the_ids():
+    w = Lora(40, 256, 136, 16, 6)
+    w.call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.call()
+    for i in range(3):
+        w.ids = torch.randint(-1, 6, (40,), generator=torch.Generator().manual_seed(i)).int()
+        w.dids.copy_(w.ids)
+        w.dD.view.zero_()
+        graph.replay()
+        got = w.check()
+        w.call()  # eager work between the replays
+        assert np.array_equal(w.dD.get().double().numpy(), got)
+
+
+def test_long_offsets():
+    """Lines so long that rows of X, A, B, C and D lie past 4 GiB."""
+    T, K, N, rank, adapters, ld = 140, 32, 40, 3, 50, 1 << 24
+    w = Lora(T, K, N, rank, adapters, BF16, F32, ids=[t % 51 - 1 for t in range(T)])
+
+    def spread(m):
+        buf = torch.empty((m.shape[0] - 1) * ld + m.shape[1], dtype=m.dtype, device="cuda")
+        torch.as_strided(buf, m.shape, (ld, 1)).copy_(m)
+        return buf
+
+    X, A, C = spread(w.X), spread(w.A), spread(w.C)
+    D = torch.empty_like(C)
+    lora = lg.GemmLora(K, N, adapters, rank, A.data_ptr(), ld, w.dB.ptr, w.dB.ld, 0, w.dscales.data_ptr())
+    ok(lg.gemm_lora_run(T, lora, X.data_ptr(), ld, w.dids.data_ptr(), C.data_ptr(), ld, D.data_ptr(), ld, BF16, F32,
+                        w.ws.data_ptr(), w.size, stream()))
+    w.dD.view.copy_(torch.as_strided(D, (T, N), (ld, 1)))
+    w.check()
