@@ -12,8 +12,7 @@ constexpr int kCkBlock = 32;  // values that share a scale
 // 2^(S - 133), the value of one unit of Q, in fp32 (below 2^-126 as a subnormal, which
 // is exact); S = 255 stands for NaN.
 __device__ __forceinline__ float ck_unit(uint32_t S) {
-    const uint32_t b = S > 6 ? (S - 6) << 23 : 0x10000u << S;
-    return __uint_as_float(S == 255 ? 0x7fc00000u : b);
+    return S == 255 ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(1.0f, (int)S - 133);
 }
 
 // Byte e of a dword as a signed integer in fp32 (one conversion that selects its byte).

@@ -296,17 +296,32 @@ inline int validate_lora_dims(int64_t T, const gemm_lora_t *l) {
     return GEMM_OK;
 }
 
-// Parts of K that different workgroups take: with few tiles of 16 tokens there are
-// CUs to spare, and an adapter's rows of A are long.
-inline int64_t lora_splits(int64_t T, int64_t K) {
-    const int64_t tiles = (T + 15) / 16, most = (K + 511) / 512;
+// Up to this many tokens they are taken 16 at a time, else 64 (lora.hpp).
+constexpr int64_t kLoraFew = 512;
+// Parts of K that different workgroups take: with few tiles of tokens there are CUs to
+// spare, and an adapter's rows of A are long.
+inline int64_t lora_splits(int64_t T, const gemm_lora_t *l) {
+    const bool few = T <= kLoraFew;
+    const int64_t tiles = few ? (T + 15) / 16 : (T + 63) / 64 * ((l->rank + 63) / 64);
+    const int64_t most = (l->K + 511) / 512;
     int64_t s = 1;
-    while (s < 8 && tiles * s < 128 && 2 * s <= most) s *= 2;
+    while (s < 8 && tiles * s < (few ? 128 : 256) && 2 * s <= most) s *= 2;
     return s;
 }
-inline int64_t lora_ldh(int64_t rank) { return (rank + 7) / 8 * 8; }
-inline int64_t lora_workspace(int64_t T, const gemm_lora_t *l) {
-    return lora_splits(T, l->K) * T * lora_ldh(l->rank) * 4 + 255;
+// Parts of the workspace, from its start rounded up to 256 bytes: the sums of each part of
+// K, and for many tokens their values of 16 bits and powers of two.
+struct LoraWorkspace {
+    int64_t splits, ldh;
+    int64_t parts, down, bytes;
+};
+inline LoraWorkspace lora_workspace(int64_t T, const gemm_lora_t *l) {
+    LoraWorkspace w;
+    w.splits = lora_splits(T, l);
+    w.ldh = (l->rank + 7) / 8 * 8;
+    w.parts = (w.splits * T * w.ldh * 4 + 255) / 256 * 256;
+    w.down = w.parts + (T > kLoraFew ? 3 * T * w.ldh * 2 : 0);
+    w.bytes = w.down + (T > kLoraFew ? 4 * T : 0) + 255;
+    return w;
 }
 
 inline int validate_lora(int64_t T, const gemm_lora_t *l, const void *X, int64_t ldx,
@@ -325,7 +340,7 @@ inline int validate_lora(int64_t T, const gemm_lora_t *l, const void *X, int64_t
         return GEMM_ERR_INVALID_LD;
     if (T == 0) return GEMM_OK;
     if (!X || !ids || !D || !workspace || !l->A || !l->B) return GEMM_ERR_NULL_PTR;
-    const int64_t need = lora_workspace(T, l);
+    const int64_t need = lora_workspace(T, l).bytes;
     if (workspace_bytes < need) return GEMM_ERR_SCRATCH_TOO_SMALL;
     const int osz = out_size(out_dtype);
     const int64_t n = l->adapters;
@@ -414,19 +429,46 @@ inline int validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int
 // The weight gradient's tiles and the parts of its tokens that different workgroups
 // take, from the sizes alone (for the 256 CUs of a whole device), so that the workspace
 // a program reserves fits whatever the device.
+//
+// Up to 64 outputs the thin kernel (bm 32, 64) streams Q: parts of at least 256 tokens
+// while there is less than a workgroup for each CU (16 x 4096 of 8192 tokens, us of the
+// kernel and the join: 8 parts 15.0, 4 18.1, 16 18.5).  Past that, the tile and the number
+// of parts with the least modelled time, in us: a workgroup's start and end, a step of 64
+// tokens (128 x 128: 0.75 alone on the GPU, 1.05 on every CU, 1.65 with two on each;
+// 256 x 256: 1.85), and the parts' sums written and read.  Measured against the model:
+// 1001 x 2056 of 3999 256 in 6 parts 51.1 (59), 128 in 3 52.8 (58), 128 in 1 69 (67);
+// 512 x 512 of 8192 128 in 12 31.0 (29), 256 in 24 33.1 (37); 4096 x 4096 of 512 256 40.0
+// (41), 128 46.9 (43).
 struct WgradPlan {
     int64_t bm, bn, splits, per;  // per: tokens of a part, a multiple of 64
 };
 inline WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
     WgradPlan w;
-    w.bm = N <= 32 ? 32 : 128;
-    w.bn = 128;
-    const int64_t tiles = ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
     const int64_t steps = (M + 63) / 64;
-    // parts of at least 4 steps while fewer than two workgroups for each CU are left
-    int64_t s = tiles > 0 ? 512 / tiles : 1;
-    if (s > steps / 4) s = steps / 4;
-    if (s > 64) s = 64;
+    int64_t s = 1;
+    if (N <= 64) {
+        w.bm = N <= 32 ? 32 : 64;
+        w.bn = 128;
+        const int64_t columns = (K + 127) / 128;
+        s = columns < 256 ? 256 / columns : 1;
+        if (s > steps / 4) s = steps / 4;
+        if (s > 64) s = 64;
+    } else {
+        double best = 0;
+        for (int64_t tile = 128; tile <= 256; tile += 128) {
+            const double tiles = (double)((N + tile - 1) / tile) * (double)((K + tile - 1) / tile);
+            for (int64_t i = 1; i <= 64 && i <= (steps > 1 ? steps / 2 : 1) && (i == 1 || tiles * i <= 1024);
+                 ++i) {
+                const double groups = tiles * i, per = (double)((steps + i - 1) / i);
+                const auto rounds = [&](double at_once) { return (double)(int64_t)((groups + at_once - 1) / at_once); };
+                double t = tile == 256    ? 14 + per * 1.85 * rounds(256)
+                           : groups <= 256 ? 10 + per * (0.75 + 0.3 * groups / 256)
+                                           : 10 + per * 1.65 * rounds(512);
+                if (i > 1) t += 3 + (double)i * (double)N * (double)K * 8 / 4.5e6;
+                if (best == 0 || t < best) best = t, w.bm = w.bn = tile, s = i;
+            }
+        }
+    }
     if (s < 1) s = 1;
     w.per = steps > 0 ? (steps + s - 1) / s * 64 : 64;
     w.splits = steps > 0 ? (steps * 64 + w.per - 1) / w.per : 1;
@@ -439,7 +481,7 @@ inline int64_t checkpoint_wgrad_workspace(int64_t M, int64_t N, int64_t K) {
         return GEMM_ERR_INVALID_DIM;
     if (M == 0 || N == 0 || K == 0) return 0;
     const WgradPlan w = wgrad_plan(M, N, K);
-    return w.splits > 1 ? w.splits * N * K * 4 + 255 : 0;
+    return w.splits > 1 ? w.splits * N * ((K + 3) / 4 * 4) * 4 + 255 : 0;
 }
 
 inline int validate_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_t ldg,

@@ -1,20 +1,23 @@
 // Low-rank adapters of many requests at once: D(t) = C(t) + s_a (x_t A_a^T) B_a^T with
-// a = ids[t], in two kernels.
+// a = ids[t].
 //
-//   lora_down_kernel: h_t = x_t A_a^T, fp32, into the workspace (parts of K by different
-//     workgroups each their own sums);
-//   lora_up_kernel: D = C + s_a h_t B_a^T.
+//   down: h_t = x_t A_a^T, fp32, into the workspace (parts of K by different workgroups
+//     each their own sums);
+//   parts (many tokens): h's parts of K added up, and split into values of 16 bits;
+//   up: D = C + s_a h_t B_a^T.
 //
-// Both take 16 consecutive tokens at a time, the columns of the 16x16x32 MFMA, whose rows
-// are rows of A (ranks) or of B (outputs).  Which adapters the tokens use is found by every
-// wave from the 16 ids: a round of the loop takes the first token left, its adapter and
-// all the tokens that share it.  Packed prompts have one round almost everywhere, and a
-// decoding batch one for each request; no sort, no list in memory, and no launch of its
-// own.  A column of an MFMA holds one token, so nothing of an adapter reaches another's
-// tokens, which take no part in the round's stores.
+// Which adapters the tokens of a tile use is found by every wave from their ids: a round
+// of the loop takes the first token left, its adapter and all the tokens that share it.
+// Packed prompts have one round almost everywhere, and a decoding batch one for each
+// request; no sort, no list in memory.  A column of an MFMA holds one token, so nothing of
+// an adapter reaches another's tokens, which take no part in the round's stores.
 //
-// What bounds both is memory: X is read once and D written once, the weights once for
-// each tile that uses them.
+// Up to kLoraFew tokens a tile is 16 of them, with a workgroup for each round, and what
+// counts is latency: two kernels, and weights straight from memory to the registers.
+// More tokens are taken 64 at a time, and what counts is the data: X and A go through LDS
+// (read in the MFMA's own shape, a lane's 16 bytes are a request of their own, 64 cycles of
+// a CU's address path for each KiB), and a wave keeps B's part in registers for its 64
+// tokens.
 #pragma once
 
 #include "stream.hpp"
@@ -31,43 +34,43 @@ struct LoraParams {
     int T, K, N, adapters, rank;
     int in_place;   // C == D: tokens without an adapter are left alone
     int vec_cd;     // 16-byte accesses to rows of C and D
-    float *h;       // [splits][T][ldh]
+    float *h;        // [splits][T][ldh]
+    uint16_t *parts; // many tokens: [parts][T][ldh], the values of 16 bits whose sum is h
+    float *down;     // many tokens, fp16: [T], the power of two that the sum is multiplied with
     int ldh, splits, k_per_split;  // k_per_split: a multiple of 128
 };
+
+// h is held as two 16-bit values for 16-bit outputs, three for fp32 ones.
+template <int OUT>
+constexpr int kLoraParts = OUT == DT_F32 ? 3 : 2;
 
 // Tokens of a tile that share an adapter.
 struct LoraGroup {
     int adapter;       // -1: tokens without one
-    uint32_t members;  // bit t: token t of the tile
+    uint64_t members;  // bit t: token t of the tile
 };
 
-// The ids of the tile's 16 tokens (lane t % 16), -1 for none, -2 past the last token.
-__device__ __forceinline__ int lora_id(const LoraParams &p, int tile, int lane) {
-    const int t = tile * 16 + (lane & 15);
-    const int id = t < p.T ? p.ids[t] : -2;
-    return t < p.T && (id < 0 || id >= p.adapters) ? -1 : id;
+// The id of lane l's token, t0 + l: -1 for none, -2 past the tile's tokens or the last one.
+__device__ __forceinline__ int lora_id(const LoraParams &p, int t0, int tokens, int lane) {
+    const int t = t0 + lane;
+    if (lane >= tokens || t >= p.T) return -2;
+    const int id = p.ids[t];
+    return id < 0 || id >= p.adapters ? -1 : id;
 }
 
 // The groups of a tile, one for each adapter in the order of their first tokens, then
 // the tokens without one: calls f(group) for groups first, first + step, ...
 template <class F>
-__device__ __forceinline__ void lora_groups(int id, int lane, int first, int step, bool none, F &&f) {
-    uint32_t left = (uint32_t)__ballot(lane < 16 && id >= 0);
-    int g = 0;
-    while (left) {
-        const int lead = __builtin_ctz(left);
-        const int a = __builtin_amdgcn_readlane(id, lead);
-        const uint32_t members = (uint32_t)__ballot(lane < 16 && id == a);
-        left &= ~members;
-        if (g == first) {
-            f(LoraGroup{a, members});
-            first += step;
-        }
-        ++g;
-    }
-    if (none && g == first) {
-        const uint32_t members = (uint32_t)__ballot(lane < 16 && id == -1);
-        if (members) f(LoraGroup{-1, members});
+__device__ __forceinline__ void lora_groups(int id, int first, int step, bool none, F &&f) {
+    uint64_t left = __ballot(id >= 0), rest = none ? __ballot(id == -1) : 0;
+    for (int g = 0; left | rest; ++g) {
+        const int a = left ? __builtin_amdgcn_readlane(id, __builtin_ctzll(left)) : -1;
+        const uint64_t members = __ballot(id == a);
+        if (left) left &= ~members;
+        else rest = 0;
+        if (g != first) continue;
+        first += step;
+        f(LoraGroup{a, members});
     }
 }
 
@@ -76,7 +79,7 @@ __device__ __forceinline__ int lora_rank(const LoraParams &p, int a) {
     return p.ranks ? min(max(uniform(p.ranks[a]), 0), p.rank) : p.rank;
 }
 
-// h of one tile and adapter at a time; a workgroup of four waves, which take
+// Few tokens: h of one tile and adapter at a time; a workgroup of four waves, which take
 // consecutive parts of its part of K.  RT row tiles of 16 ranks at once.
 // Grid: x tiles, y groups of a tile, z parts of K times chunks of 16 RT ranks.
 template <int IT, int RT, bool VEC>
@@ -84,13 +87,13 @@ __global__ void __launch_bounds__(256) lora_down_kernel(LoraParams p) {
     __shared__ f32x4 part[3][RT][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int split = blockIdx.z % p.splits, r0 = blockIdx.z / p.splits * 16 * RT;
-    const int id = lora_id(p, blockIdx.x, lane);
+    const int id = lora_id(p, blockIdx.x * 16, 16, lane);
     const int t = blockIdx.x * 16 + (lane & 15), chunk = 8 * (lane >> 4);
     const uint8_t *x = p.X + (int64_t)min(t, p.T - 1) * p.ldx * 2;
     const int k_end = min(p.K, (split + 1) * p.k_per_split);
     const int per = p.k_per_split / 4, kb = split * p.k_per_split + wave * per;
     const int ke = min(k_end, kb + per);
-    lora_groups(id, lane, blockIdx.y, gridDim.y, false, [&](const LoraGroup &g) {
+    lora_groups(id, blockIdx.y, gridDim.y, false, [&](const LoraGroup &g) {
         const int rank = lora_rank(p, g.adapter);
         // (rows past the adapter's rank read its first; their sums are not kept)
         const uint8_t *a[RT];
@@ -151,172 +154,361 @@ __global__ void __launch_bounds__(256) lora_down_kernel(LoraParams p) {
     });
 }
 
+// Many tokens: h of 64 tokens and 16 RT ranks.  64 values of k at a time through four LDS
+// stages, three of them on their way; a wave takes 16 of the tokens.
+// Grid: x tiles, y chunks of 16 RT ranks, z parts of K.
+template <int IT, int RT>
+__global__ void __launch_bounds__(256) lora_down_tile_kernel(LoraParams p) {
+    constexpr int ROWS = 64 + 16 * RT, STAGES = 4, NL = ROWS * 8 / 256;  // 8 chunks of 16 bytes a row
+    static_assert(ROWS * 8 % 256 == 0, "whole loads of 64 chunks for each wave");
+    __shared__ u32x4 smem[STAGES * ROWS * 8];
+    char *const lds = reinterpret_cast<char *>(smem);
+    const uint32_t lds_base = (uint32_t)(uintptr_t)(LIBGEMM_LDS char *)lds;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int t0 = blockIdx.x * 64, r0 = blockIdx.y * 16 * RT;
+    const int kb = blockIdx.z * p.k_per_split, ke = min(p.K, kb + p.k_per_split);
+    const int steps = ke > kb ? (ke - kb) / 64 : 0;  // whole ones; the rest straight from memory
+    const int id = lora_id(p, t0, 64, lane);
+    const int mine = t0 + 16 * wave + (lane & 15);  // this lane's token
+    const uint8_t *const x = p.X + (int64_t)min(mine, p.T - 1) * p.ldx * 2;
+    lora_groups(id, 0, 1, false, [&](const LoraGroup &g) {
+        const int rank = lora_rank(p, g.adapter);
+        const uint8_t *const a0 = p.A + (int64_t)g.adapter * p.rank * p.lda * 2;
+        f32x4 acc[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (r0 < rank) {
+            // load i of the wave: rows 0 to 63 of a stage are tokens, the others ranks.  Rows
+            // past the last token read it, rows past the rank read rank 0: columns that are
+            // not kept
+            const uint8_t *src[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int q = (wave * NL + i) * 64 + lane, row = q / 8, c = (q % 8) ^ swz_kc(row);
+                const int r = r0 + row - 64;
+                const uint8_t *line = row < 64 ? p.X + (int64_t)min(t0 + row, p.T - 1) * p.ldx * 2
+                                               : a0 + (int64_t)(r < rank ? r : 0) * p.lda * 2;
+                src[i] = line + (kb + 8 * c) * 2;
+            }
+            // Step n of k into stage s.  (Written out: the compiler would let every LDS read
+            // behind the builtin wait for it.  Nothing else here uses m0.)
+            auto load = [&](int n, int s) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const uint32_t dst = lds_base + ((s % STAGES) * ROWS * 8 + (wave * NL + i) * 64) * 16;
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                                 :
+                                 : "s"(uniform((int)dst)), "v"(src[i] + n * 128)
+                                 : "memory");
+                }
+            };
+            // (past the last step the loads go on, so that the waits' counts hold)
+            const int last = steps - 1;
+            if (steps > 0) {
+#pragma unroll
+                for (int s = 0; s < STAGES - 1; ++s) load(min(s, last), s);
+            }
+            const int lg = kc_group16(lane >> 4);
+            for (int s = 0; s < steps; ++s) {
+                wait_vmcnt<(STAGES - 2) * NL>();  // step s is there
+                __syncthreads();                  // everywhere, and stage s - 1 is read
+                load(min(s + STAGES - 1, last), s + STAGES - 1);
+                const char *const st = lds + (s % STAGES) * ROWS * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    auto frag = [&](int row) {
+                        return *reinterpret_cast<const u32x4 *>(st + (row * 8 + ((4 * h + lg) ^ swz_kc(row))) * 16);
+                    };
+                    const u32x4 xv = frag(16 * wave + (lane & 15));
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        acc[i] = mfma16_1<IT>(frag(64 + 16 * i + (lane & 15)), xv, acc[i]);
+                }
+            }
+            wait_vmcnt<0>();
+            for (int k = kb + 64 * steps + 8 * (lane >> 4); k - 8 * (lane >> 4) < ke; k += 32) {
+                const u32x4 xv = stream_chunk<2, true>(x, k, ke);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const int r = r0 + 16 * i + (lane & 15);
+                    acc[i] = mfma16_1<IT>(
+                        stream_chunk<2, true>(a0 + (int64_t)(r < rank ? r : 0) * p.lda * 2, k, ke), xv, acc[i]);
+                }
+            }
+            __syncthreads();  // the stages are read
+        }
+        if (g.members >> (16 * wave + (lane & 15)) & 1) {
+            float *h = p.h + ((int64_t)blockIdx.z * p.T + mine) * p.ldh;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int r = r0 + 16 * i + 4 * (lane >> 4);
+                f32x4 v = acc[i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = r + e < rank ? v[e] : 0.0f;
+                if (r < p.ldh) *reinterpret_cast<f32x4 *>(h + r) = v;
+            }
+        }
+    });
+}
+
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float lora_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// D of one tile and adapter at a time: a wave takes 64 columns.  Its four row tiles
-// interleave the columns by fours, so that a lane ends up with 16 consecutive ones:
-// row i of tile j is column 16 (i / 4) + 4 j + i % 4.
-//
-// h goes into the MFMA as PARTS values of the 16-bit type, laid end to end along the
-// product's depth (a rank of 16 in two parts fills its 32 exactly), B's row being read
-// once for each part.  fp16 parts are those of h times a power of two that brings the
-// token's largest |h| to [2^8, 2^9).
-// Grid: x tiles, y groups of a tile, z blocks of 256 columns.
-template <int IT, int OUT, bool VEC>
-__global__ void __launch_bounds__(256) lora_up_kernel(LoraParams p) {
-    constexpr int PARTS = OUT == DT_F32 ? 3 : 2;
+// fp16: the exponent that brings a token's largest |h| to [2^8, 2^9).  (A largest value
+// below 2^-118 is taken as that; Inf and NaN stay so.)
+__device__ __forceinline__ int lora_exponent(float m) {
+    const int e = (int)(__float_as_uint(m) >> 23) - 127;
+    return min(max(8 - e, -119), 126);
+}
+
+// Eight values (times a power of two) as PARTS 16-bit values each whose sum they are.  A
+// value that is not finite has no rest.
+template <int IT, int PARTS>
+__device__ __forceinline__ void lora_split(const float (&v)[8], float up, u32x4 (&w)[PARTS]) {
     constexpr int DT = IT == IT_F16 ? DT_F16 : DT_BF16;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float a = IT == IT_F16 ? v[e] * up : v[e], b = IT == IT_F16 ? v[e + 1] * up : v[e + 1];
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            uint32_t x = to_out16<DT>(a, false), y = to_out16<DT>(b, false);
+            if (q > 0) {
+                x = a != a ? 0u : x;
+                y = b != b ? 0u : y;
+            }
+            w[q][e / 2] = x | (y << 16);
+            a -= from_out16<DT>(x);
+            b -= from_out16<DT>(y);
+        }
+    }
+}
+
+// The sum of h's parts of K, ranks 8c .. 8c + 7 of token t; all loads before the first
+// addition.
+__device__ __forceinline__ void lora_load_h(const LoraParams &p, int64_t t, int c, float (&v)[8]) {
+    const int64_t part = (int64_t)p.T * p.ldh;
+    const float *h = p.h + t * p.ldh + 8 * c;
+    f32x4 w[8][2];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        if (s < p.splits) {
+            w[s][0] = *reinterpret_cast<const f32x4 *>(h + s * part);
+            w[s][1] = *reinterpret_cast<const f32x4 *>(h + s * part + 4);
+        }
+    f32x4 a = w[0][0], b = w[0][1];
+#pragma unroll
+    for (int s = 1; s < 8; ++s)
+        if (s < p.splits) a += w[s][0], b += w[s][1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+}
+
+// Many tokens: a thread takes 8 ranks of a token, 32 (or fewer) threads a token.
+template <int IT, int PARTS>
+__global__ void __launch_bounds__(256) lora_parts_kernel(LoraParams p, int lanes) {
+    const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    const int c = threadIdx.x % lanes;
+    const bool in = t < p.T && 8 * c < p.ldh;
+    float v[8], m = 0.0f, up = 1.0f;
+    // (a token without an adapter has no h: what is there is split, and not used)
+    if (in) lora_load_h(p, t, c, v);
+    if constexpr (IT == IT_F16) {
+        if (in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
+        }
+        for (int s = 1; s < lanes; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
+        const int by = lora_exponent(m);
+        up = lora_pow2(by);
+        if (in && c == 0) p.down[t] = lora_pow2(-by);
+    }
+    if (!in) return;
+    u32x4 w[PARTS];
+    lora_split<IT, PARTS>(v, up, w);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+        *reinterpret_cast<u32x4 *>(p.parts + ((int64_t)q * p.T + t) * p.ldh + 8 * c) = w[q];
+}
+
+// 16 values of a row of C or D, as many as n.
+template <int OUT>
+__device__ __forceinline__ void lora_load16(const uint8_t *p, int64_t at, int n, bool vec, float (&y)[16]) {
     constexpr int OSZ = OUT == DT_F32 ? 4 : 2;
+    if (vec && n == 16) {
+        const u32x4 *c = reinterpret_cast<const u32x4 *>(p + at * OSZ);
+#pragma unroll
+        for (int q = 0; q < OSZ; ++q) {
+            const u32x4 w = c[q];
+            if constexpr (OUT == DT_F32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[4 * q + e] = __uint_as_float(w[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[8 * q + e] = from_out16<OUT>(half_of(w, e));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            y[e] = 0.0f;
+            if (e < n) {
+                if constexpr (OUT == DT_F32) y[e] = reinterpret_cast<const float *>(p)[at + e];
+                else y[e] = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p)[at + e]);
+            }
+        }
+    }
+}
+template <int OUT>
+__device__ __forceinline__ void lora_store16(uint8_t *p, int64_t at, int n, bool vec, const float (&y)[16]) {
+    if constexpr (OUT == DT_F32) {
+        float *d = reinterpret_cast<float *>(p) + at;
+        if (vec && n == 16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                reinterpret_cast<f32x4 *>(d)[q] = f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e < n) d[e] = y[e];
+        }
+    } else {
+        uint16_t *d = reinterpret_cast<uint16_t *>(p) + at;
+        if (vec && n == 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_out16<OUT>(y[2 * e], y[2 * e + 1]);
+            reinterpret_cast<u32x4 *>(d)[0] = u32x4{w[0], w[1], w[2], w[3]};
+            reinterpret_cast<u32x4 *>(d)[1] = u32x4{w[4], w[5], w[6], w[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e < n) d[e] = (uint16_t)to_out16<OUT>(y[e], false);
+        }
+    }
+}
+
+// D of one tile and adapter at a time: SUBS times 16 tokens; a wave takes 64 columns.  Its
+// four row tiles interleave the columns by fours, so that a lane ends up with 16
+// consecutive ones: row i of tile j is column 16 (i / 4) + 4 j + i % 4.
+//
+// h goes into the MFMA as its 16-bit values, one MFMA after the other on the same part of
+// B, 32 RS ranks at a time.  SUBS == 1: few tokens, h's parts of K are added up and split
+// here.  SUBS == 4: many, they have been.
+// Grid: x tiles, y groups of a tile, z blocks of 256 columns.
+template <int IT, int OUT, int SUBS, int RS, bool VEC>
+__global__ void __launch_bounds__(256, 2) lora_up_kernel(LoraParams p) {
+    constexpr int PARTS = kLoraParts<OUT>;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.z * 256 + wave * 64;
     if (n0 >= p.N) return;
-    const int id = lora_id(p, blockIdx.x, lane);
-    const int t = blockIdx.x * 16 + (lane & 15), lg = lane >> 4;
+    const int t0 = blockIdx.x * 16 * SUBS, lg = lane >> 4;
+    const int id = lora_id(p, t0, 16 * SUBS, lane);
     const int64_t n = n0 + 16 * lg;  // this lane's 16 columns
     const int left = (int)min(max(p.N - n, (int64_t)0), (int64_t)16);
     const int chunks = p.ldh / 8;    // of 8 ranks
-    lora_groups(id, lane, blockIdx.y, gridDim.y, !p.in_place, [&](const LoraGroup &g) {
-        f32x4 acc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto token = [&](int s) { return t0 + 16 * s + (lane & 15); };
+    // what does not depend on the ids is asked for before they are there
+    float y0[16];
+    u32x4 hv0[PARTS];
+    float down0 = 1.0f;
+    if constexpr (SUBS == 1) {
+        const int t = min(token(0), p.T - 1);
+        if (p.C) lora_load16<OUT>(p.C, (int64_t)t * p.ldc + n, left, p.vec_cd, y0);
+    }
+    lora_groups(id, blockIdx.y, gridDim.y, !p.in_place, [&](const LoraGroup &g) {
         const int rank = g.adapter < 0 ? 0 : lora_rank(p, g.adapter);
-        const bool member = g.members >> (lane & 15) & 1;
-        float scale = 0.0f, down = 1.0f;
-        if (rank > 0) {
-            scale = p.scales ? p.scales[g.adapter] : 1.0f;
-            const float *h = p.h + (int64_t)(member ? t : blockIdx.x * 16) * p.ldh;
-            const int64_t part = (int64_t)p.T * p.ldh;
-            auto load_h = [&](int c, float (&v)[8]) {
-                f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-                if (member) {
-                    for (int s = 0; s < p.splits; ++s) {
-                        a += *reinterpret_cast<const f32x4 *>(h + s * part + 8 * c);
-                        b += *reinterpret_cast<const f32x4 *>(h + s * part + 8 * c + 4);
-                    }
-                }
+        const float scale = rank > 0 && p.scales ? p.scales[g.adapter] : 1.0f;
+        f32x4 acc[SUBS][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-            };
-            float up = 1.0f;
-            if constexpr (IT == IT_F16) {
+        for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[s][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        float up = 1.0f;
+        const bool in0 = g.members >> (lane & 15) & 1;
+        if constexpr (SUBS == 1 && IT == IT_F16) {
+            if (rank > 0) {
                 float m = 0.0f;
-                for (int c = lg; c < chunks; c += 4) {
-                    float v[8];
-                    load_h(c, v);
+                if (in0)
+                    for (int c = lg; c < chunks; c += 4) {
+                        float v[8];
+                        lora_load_h(p, token(0), c, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
-                }
+                        for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
+                    }
                 m = fmaxf(m, __shfl_xor(m, 16));
                 m = fmaxf(m, __shfl_xor(m, 32));
-                // (a largest value below 2^-118 is taken as that; Inf and NaN stay so)
-                const int e = (int)(__float_as_uint(m) >> 23) - 127;
-                const int by = min(max(8 - e, -119), 126);
+                const int by = lora_exponent(m);
                 up = lora_pow2(by);
-                down = lora_pow2(-by);
+                down0 = lora_pow2(-by);
             }
-            const uint8_t *b[4];
+        }
+        const uint8_t *b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t col = n0 + 16 * ((lane & 15) >> 2) + 4 * j + (lane & 3);
-                b[j] = p.B + ((int64_t)g.adapter * p.N + (col < p.N ? col : p.N - 1)) * p.ldb * 2;
-            }
-            for (int c0 = 0; c0 < PARTS * chunks; c0 += 4) {
-                const int c = c0 + lg;
-                const int which = c / chunks, rc = c - which * chunks;
-                const bool used = which < PARTS;
-                float v[8];
-                u32x4 hv = {0u, 0u, 0u, 0u};
-                if (used) {
-                    load_h(rc, v);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t col = n0 + 16 * ((lane & 15) >> 2) + 4 * j + (lane & 3);
+            b[j] = p.B + ((int64_t)max(g.adapter, 0) * p.N + (col < p.N ? col : p.N - 1)) * p.ldb * 2;
+        }
+        for (int r0 = 0; r0 < rank; r0 += 32 * RS) {
+            u32x4 bv[RS][4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float x = v[e] * up;
-                        uint32_t w = to_out16<DT>(x, false);
+            for (int q = 0; q < RS; ++q)
 #pragma unroll
-                        for (int q = 1; q < PARTS; ++q) {
-                            if (q <= which) {
-                                x -= from_out16<DT>(w);
-                                w = to_out16<DT>(x, false);
-                            }
+                for (int j = 0; j < 4; ++j) bv[q][j] = stream_chunk<2, VEC>(b[j], r0 + 32 * q + 8 * lg, rank);
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s) {
+                if (!(g.members >> (16 * s) & 0xffff)) continue;
+                const bool in = g.members >> (16 * s + (lane & 15)) & 1;
+#pragma unroll
+                for (int q = 0; q < RS; ++q) {
+                    const int c = r0 / 8 + 4 * q + lg;
+                    const bool used = in && c < chunks;
+                    if constexpr (SUBS == 1) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                        if (used) lora_load_h(p, token(s), c, v);
+                        lora_split<IT, PARTS>(v, up, hv0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < PARTS; ++k) {
+                            hv0[k] = u32x4{0u, 0u, 0u, 0u};
+                            if (used)
+                                hv0[k] = *reinterpret_cast<const u32x4 *>(
+                                    p.parts + ((int64_t)k * p.T + token(s)) * p.ldh + 8 * c);
                         }
-                        // (a value that is not finite has no rest)
-                        if (which > 0 && x != x) w = 0u;
-                        hv[e / 2] |= w << (16 * (e % 2));
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[j] = mfma16_1<IT>(stream_chunk<2, VEC>(b[j], used ? 8 * rc : rank, rank), hv,
-                                          acc[j]);
-            }
-        }
-        if (!member || left == 0) return;
-        float y[16];
-        const int64_t co = (int64_t)t * p.ldc + n, d_o = (int64_t)t * p.ldd + n;
-        if (!p.C) {
+                    for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-        } else if (p.vec_cd && left == 16) {
-            const u32x4 *c = reinterpret_cast<const u32x4 *>(p.C + co * OSZ);
-#pragma unroll
-            for (int q = 0; q < 2 * OSZ / 2; ++q) {
-                const u32x4 w = c[q];
-                if constexpr (OUT == DT_F32) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[4 * q + e] = __uint_as_float(w[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[8 * q + e] = from_out16<OUT>(half_of(w, e));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                y[e] = 0.0f;
-                if (e < left) {
-                    if constexpr (OUT == DT_F32)
-                        y[e] = reinterpret_cast<const float *>(p.C)[co + e];
-                    else
-                        y[e] = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p.C)[co + e]);
+                        for (int j = 0; j < 4; ++j) acc[s][j] = mfma16_1<IT>(bv[q][j], hv0[k], acc[s][j]);
                 }
             }
         }
-        if (rank > 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float v = acc[e / 4][e % 4];
-                y[e] += scale * (IT == IT_F16 ? v * down : v);
-            }
-        }
-        if constexpr (OUT == DT_F32) {
-            float *d = reinterpret_cast<float *>(p.D) + d_o;
-            if (p.vec_cd && left == 16) {
+        for (int s = 0; s < SUBS; ++s) {
+            if (!(g.members >> (16 * s + (lane & 15)) & 1) || left == 0) continue;
+            const int64_t t = token(s);
+            float y[16], by = 1.0f;
+            if constexpr (SUBS == 1) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    reinterpret_cast<f32x4 *>(d)[q] =
-                        f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+                for (int e = 0; e < 16; ++e) y[e] = y0[e];
+                by = down0;
             } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < left) d[e] = y[e];
+                if (p.C) lora_load16<OUT>(p.C, t * p.ldc + n, left, p.vec_cd, y);
+                if (IT == IT_F16 && rank > 0) by = p.down[t];
             }
-        } else {
-            uint16_t *d = reinterpret_cast<uint16_t *>(p.D) + d_o;
-            uint32_t w[16];
+            if (!p.C) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = to_out16<OUT>(y[e], false);
-            if (p.vec_cd && left == 16) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    reinterpret_cast<u32x4 *>(d)[q] =
-                        u32x4{w[8 * q] | (w[8 * q + 1] << 16), w[8 * q + 2] | (w[8 * q + 3] << 16),
-                              w[8 * q + 4] | (w[8 * q + 5] << 16), w[8 * q + 6] | (w[8 * q + 7] << 16)};
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < left) d[e] = (uint16_t)w[e];
+                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
             }
+            if (rank > 0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float v = acc[s][e / 4][e % 4];
+                    y[e] += scale * (IT == IT_F16 ? v * by : v);
+                }
+            }
+            lora_store16<OUT>(p.D, t * p.ldd + n, left, p.vec_cd, y);
         }
     });
 }

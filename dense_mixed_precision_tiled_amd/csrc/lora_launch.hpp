@@ -1,0 +1,71 @@
+// The launches of gemm_lora_run, instantiated for each type of its inputs.
+#pragma once
+
+#include "gemm_host.hpp"
+#include "lora.hpp"
+
+namespace libgemm {
+
+template <int IT, int OUT, int SUBS, bool VEC>
+const void *lora_up_of(int rank) {
+    return rank <= 32 ? (const void *)lora_up_kernel<IT, OUT, SUBS, 1, VEC>
+                      : (const void *)lora_up_kernel<IT, OUT, SUBS, 2, VEC>;
+}
+template <int IT, int SUBS, bool VEC>
+const void *lora_up_of(int out_dtype, int rank) {
+    return out_dtype == DT_F32   ? lora_up_of<IT, DT_F32, SUBS, VEC>(rank)
+           : out_dtype == DT_F16 ? lora_up_of<IT, DT_F16, SUBS, VEC>(rank)
+                                 : lora_up_of<IT, DT_BF16, SUBS, VEC>(rank);
+}
+template <int IT, int RT>
+const void *lora_down_of(bool vec) {
+    return vec ? (const void *)lora_down_kernel<IT, RT, true> : (const void *)lora_down_kernel<IT, RT, false>;
+}
+
+// few: 16 tokens at a time.  vec_xa, vec_b: 16-byte loads of X and A, and of B.  Many
+// tokens without vec_xa take the first kernel of the few: its loads know any alignment.
+template <int IT>
+hipError_t launch_lora(const LoraParams &p, int out_dtype, bool few, bool vec_xa, bool vec_b,
+                       hipStream_t s) {
+    using libgemm_host::cdiv;
+    LoraParams arg = p;
+    void *args[] = {&arg};
+    // ranks taken at once: 16, 32 or 64
+    const int rt = p.rank <= 16 ? 1 : p.rank <= 32 ? 2 : 4;
+    const unsigned chunks = (unsigned)cdiv(p.rank, 16 * rt);
+    const unsigned tiles16 = (unsigned)cdiv(p.T, 16), tiles64 = (unsigned)cdiv(p.T, 64);
+    // a workgroup for each group that a tile may hold while tiles are few
+    const unsigned groups = few ? (unsigned)(p.T < 16 ? p.T : 16) : 1;
+    hipError_t e;
+    if (few || !vec_xa) {
+        const void *k = rt == 1   ? lora_down_of<IT, 1>(vec_xa)
+                        : rt == 2 ? lora_down_of<IT, 2>(vec_xa)
+                                  : lora_down_of<IT, 4>(vec_xa);
+        e = hipLaunchKernel(k, dim3(tiles16, groups, (unsigned)p.splits * chunks), dim3(256), args, 0, s);
+    } else {
+        const void *k = rt < 4 ? (const void *)lora_down_tile_kernel<IT, 2>
+                               : (const void *)lora_down_tile_kernel<IT, 4>;
+        e = hipLaunchKernel(k, dim3(tiles64, chunks, (unsigned)p.splits), dim3(256), args, 0, s);
+    }
+    if (e != hipSuccess) return e;
+    const dim3 grid(few ? tiles16 : tiles64, groups, (unsigned)cdiv(p.N, 256));
+    if (few) {
+        const void *k = vec_b ? lora_up_of<IT, 1, true>(out_dtype, p.rank)
+                              : lora_up_of<IT, 1, false>(out_dtype, p.rank);
+        return hipLaunchKernel(k, grid, dim3(256), args, 0, s);
+    }
+    int lanes = 1;  // threads of a token, 8 ranks each
+    while (8 * lanes < p.ldh) lanes *= 2;
+    void *with_lanes[] = {&arg, &lanes};
+    const void *k = out_dtype == DT_F32 ? (const void *)lora_parts_kernel<IT, 3>
+                                        : (const void *)lora_parts_kernel<IT, 2>;
+    e = hipLaunchKernel(k, dim3((unsigned)cdiv(p.T, 256 / lanes)), dim3(256), with_lanes, 0, s);
+    if (e != hipSuccess) return e;
+    k = vec_b ? lora_up_of<IT, 4, true>(out_dtype, p.rank) : lora_up_of<IT, 4, false>(out_dtype, p.rank);
+    return hipLaunchKernel(k, grid, dim3(256), args, 0, s);
+}
+
+hipError_t launch_lora_f16(const LoraParams &, int out_dtype, bool few, bool vec_xa, bool vec_b, hipStream_t);
+hipError_t launch_lora_bf16(const LoraParams &, int out_dtype, bool few, bool vec_xa, bool vec_b, hipStream_t);
+
+}  // namespace libgemm
