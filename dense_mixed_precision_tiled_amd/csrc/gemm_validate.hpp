@@ -296,16 +296,21 @@ inline int validate_lora_dims(int64_t T, const gemm_lora_t *l) {
     return GEMM_OK;
 }
 
-// Up to this many tokens they are taken 16 at a time, else 64 (lora.hpp).
-constexpr int64_t kLoraFew = 512;
+// Up to this many tokens they are taken one by one and 16 at a time, else 64 (lora.hpp).
+// us on 4096 x 4096 in bf16, first against second way: packed prompts of 4 adapters, 128
+// tokens, rank 16 11.7 and 20.1, rank 64 25 and 24; 256 tokens 18.4 and 16.4, 41 and 19; 512
+// tokens 24 and 17, 59 and 19.  Tokens of 32 adapters in any order, as a decoding batch has
+// them: 256 tokens 21 and 167, 53 and 217; 512 tokens 33 and 170, 90 and 234.
+constexpr int64_t kLoraFew = 256;
 // Parts of K that different workgroups take: with few tiles of tokens there are CUs to
 // spare, and an adapter's rows of A are long.
 inline int64_t lora_splits(int64_t T, const gemm_lora_t *l) {
     const bool few = T <= kLoraFew;
-    const int64_t tiles = few ? (T + 15) / 16 : (T + 63) / 64 * ((l->rank + 63) / 64);
+    // (few: as many groups as tokens, at the most)
+    const int64_t tiles = few ? T : (T + 63) / 64 * ((l->rank + 63) / 64);
     const int64_t most = (l->K + 511) / 512;
     int64_t s = 1;
-    while (s < 8 && tiles * s < (few ? 128 : 256) && 2 * s <= most) s *= 2;
+    while (s < 4 && tiles * s < 256 && 2 * s <= most) s *= 2;
     return s;
 }
 // Parts of the workspace, from its start rounded up to 256 bytes: the sums of each part of

@@ -12,12 +12,16 @@
 // request; no sort, no list in memory.  A column of an MFMA holds one token, so nothing of
 // an adapter reaches another's tokens, which take no part in the round's stores.
 //
-// Up to kLoraFew tokens a tile is 16 of them, with a workgroup for each round, and what
-// counts is latency: two kernels, and weights straight from memory to the registers.
-// More tokens are taken 64 at a time, and what counts is the data: X and A go through LDS
-// (read in the MFMA's own shape, a lane's 16 bytes are a request of their own, 64 cycles of
-// a CU's address path for each KiB), and a wave keeps B's part in registers for its 64
-// tokens.
+// Up to kLoraFew tokens (a decoding batch) what counts is latency: two kernels, weights
+// straight from memory to the registers, the first 16 tokens and an adapter for each
+// workgroup, the second a token for each wave.  More tokens (prompts) are taken 64 at a
+// time, and what counts is the data: X and A go through LDS (read in the MFMA's own shape,
+// a lane's 16 bytes are a request of their own, 64 cycles of a CU's address path for each
+// KiB), and a wave keeps B's part in registers for its 64 tokens.
+//
+// Kernels on 4096 x 4096 in bf16, us: one token, rank 16, 3.7 and 3.5; 64 tokens of 64
+// adapters 5.9 and 4.6 (16.8 MB of weights); 4096 tokens, rank 64, 8 adapters 16.2, 4.8 and
+// 26.9 (2.1 and 2.5 TB/s).
 #pragma once
 
 #include "stream.hpp"
@@ -283,21 +287,21 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], float up, u32x4 
     }
 }
 
-// The sum of h's parts of K, ranks 8c .. 8c + 7 of token t; all loads before the first
-// addition.
+// The sum of h's parts of K (four at most), ranks 8c .. 8c + 7 of token t; all loads
+// before the first addition.
 __device__ __forceinline__ void lora_load_h(const LoraParams &p, int64_t t, int c, float (&v)[8]) {
     const int64_t part = (int64_t)p.T * p.ldh;
     const float *h = p.h + t * p.ldh + 8 * c;
-    f32x4 w[8][2];
+    f32x4 w[4][2];
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
+    for (int s = 0; s < 4; ++s)
         if (s < p.splits) {
             w[s][0] = *reinterpret_cast<const f32x4 *>(h + s * part);
             w[s][1] = *reinterpret_cast<const f32x4 *>(h + s * part + 4);
         }
     f32x4 a = w[0][0], b = w[0][1];
 #pragma unroll
-    for (int s = 1; s < 8; ++s)
+    for (int s = 1; s < 4; ++s)
         if (s < p.splits) a += w[s][0], b += w[s][1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
@@ -330,31 +334,23 @@ __global__ void __launch_bounds__(256) lora_parts_kernel(LoraParams p, int lanes
         *reinterpret_cast<u32x4 *>(p.parts + ((int64_t)q * p.T + t) * p.ldh + 8 * c) = w[q];
 }
 
-// 16 values of a row of C or D, as many as n.
+// 16 values of a row of C or D, as many as n: from 16-byte loads, or one by one.
 template <int OUT>
-__device__ __forceinline__ void lora_load16(const uint8_t *p, int64_t at, int n, bool vec, float (&y)[16]) {
-    constexpr int OSZ = OUT == DT_F32 ? 4 : 2;
-    if (vec && n == 16) {
-        const u32x4 *c = reinterpret_cast<const u32x4 *>(p + at * OSZ);
+__device__ __forceinline__ void lora_values(const u32x4 (&w)[OUT == DT_F32 ? 4 : 2], float (&y)[16]) {
 #pragma unroll
-        for (int q = 0; q < OSZ; ++q) {
-            const u32x4 w = c[q];
-            if constexpr (OUT == DT_F32) {
+    for (int e = 0; e < 16; ++e) {
+        if constexpr (OUT == DT_F32) y[e] = __uint_as_float(w[e / 4][e % 4]);
+        else y[e] = from_out16<OUT>(half_of(w[e / 8], e % 8));
+    }
+}
+template <int OUT>
+__device__ __forceinline__ void lora_load_some(const uint8_t *p, int64_t at, int n, float (&y)[16]) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[4 * q + e] = __uint_as_float(w[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[8 * q + e] = from_out16<OUT>(half_of(w, e));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            y[e] = 0.0f;
-            if (e < n) {
-                if constexpr (OUT == DT_F32) y[e] = reinterpret_cast<const float *>(p)[at + e];
-                else y[e] = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p)[at + e]);
-            }
+    for (int e = 0; e < 16; ++e) {
+        y[e] = 0.0f;
+        if (e < n) {
+            if constexpr (OUT == DT_F32) y[e] = reinterpret_cast<const float *>(p)[at + e];
+            else y[e] = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p)[at + e]);
         }
     }
 }
@@ -387,125 +383,159 @@ __device__ __forceinline__ void lora_store16(uint8_t *p, int64_t at, int n, bool
     }
 }
 
-// D of one tile and adapter at a time: SUBS times 16 tokens; a wave takes 64 columns.  Its
-// four row tiles interleave the columns by fours, so that a lane ends up with 16
-// consecutive ones: row i of tile j is column 16 (i / 4) + 4 j + i % 4.
+// Few tokens: D of one token, 64 columns for a wave.  A column is a lane's dot product of
+// rank terms, in fp32 with h as it is: with a token an adapter, a column of the MFMA would
+// be all that it uses of one (64 tokens of 64 adapters, 4096 columns: 10.0 us so, and 5 us
+// with a token for each wave).
+// Grid: x blocks of 256 columns, y tokens.
+template <int IT, int OUT, bool VEC>
+__global__ void __launch_bounds__(256) lora_up_few_kernel(LoraParams p) {
+    const int lane = threadIdx.x & 63, t = blockIdx.y;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, row = min(n, (int64_t)p.N - 1);
+    const int id = uniform(p.ids[t]);
+    const bool has = id >= 0 && id < p.adapters;
+    if (!has && p.in_place) return;
+    auto c_at = [&](int64_t at) {
+        if constexpr (OUT == DT_F32) return reinterpret_cast<const float *>(p.C)[at];
+        else return from_out16<OUT>(reinterpret_cast<const uint16_t *>(p.C)[at]);
+    };
+    const float c = p.C ? c_at((int64_t)t * p.ldc + row) : 0.0f;
+    float y = c;
+    const int rank = has ? lora_rank(p, id) : 0;
+    if (rank > 0) {
+        const float scale = p.scales ? p.scales[id] : 1.0f;
+        const uint8_t *b = p.B + ((int64_t)id * p.N + row) * p.ldb * 2;
+        const float *h = p.h + (int64_t)t * p.ldh;
+        const int64_t part = (int64_t)p.T * p.ldh;
+        float dot = 0.0f;
+        for (int r0 = 0; r0 < rank; r0 += 64) {
+            // lane l holds rank r0 + l, 0 past the adapter's (where B is masked too)
+            float mine = 0.0f;
+            if (r0 + lane < p.ldh) {
+                float w[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) w[s] = s < p.splits ? h[s * part + r0 + lane] : 0.0f;
+                mine = w[0];
+#pragma unroll
+                for (int s = 1; s < 4; ++s)
+                    if (s < p.splits) mine += w[s];
+            }
+            const int chunks = min(8, (rank - r0 + 7) / 8);
+            for (int k = 0; k < chunks; k += 2) {
+                // (past the last chunk: the row's first, masked)
+                u32x4 v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) v[e] = stream_chunk<2, VEC>(b, r0 + 8 * (k + e), rank);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float x = from_out16<IT == IT_F16 ? DT_F16 : DT_BF16>(half_of(v[e / 8], e % 8));
+                    const float g = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+                        (int)__float_as_uint(mine), min(8 * k + e, 63)));
+                    // (a masked term is 0 * 0, also where h is not finite)
+                    dot = __builtin_fmaf(x, r0 + 8 * k + e < rank ? g : 0.0f, dot);
+                }
+            }
+        }
+        y = __builtin_fmaf(scale, dot, c);
+    }
+    if (n >= p.N) return;
+    const int64_t at = (int64_t)t * p.ldd + n;
+    if constexpr (OUT == DT_F32) reinterpret_cast<float *>(p.D)[at] = y;
+    else reinterpret_cast<uint16_t *>(p.D)[at] = (uint16_t)to_out16<OUT>(y, false);
+}
+
+// Many tokens: D of 64 tokens and an adapter at a time; a wave takes 64 columns.  Its four
+// row tiles interleave the columns by fours, so that a lane ends up with 16 consecutive
+// ones: row i of tile j is column 16 (i / 4) + 4 j + i % 4.
 //
 // h goes into the MFMA as its 16-bit values, one MFMA after the other on the same part of
-// B, 32 RS ranks at a time.  SUBS == 1: few tokens, h's parts of K are added up and split
-// here.  SUBS == 4: many, they have been.
-// Grid: x tiles, y groups of a tile, z blocks of 256 columns.
-template <int IT, int OUT, int SUBS, int RS, bool VEC>
+// B.  B's 32 RS ranks stay in registers for the tile's tokens (larger ranks read B for
+// every 16 tokens).  C, which no id decides, is asked for first.
+// Grid: x blocks of 256 columns (so that an XCD's L2 holds few blocks of B: 27.4 us, tiles
+// first 29.3), z tiles.
+template <int IT, int OUT, int RS, bool VEC>
 __global__ void __launch_bounds__(256, 2) lora_up_kernel(LoraParams p) {
-    constexpr int PARTS = kLoraParts<OUT>;
+    constexpr int SUBS = 4, PARTS = kLoraParts<OUT>, CW = OUT == DT_F32 ? 4 : 2, OSZ = CW;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t n0 = (int64_t)blockIdx.z * 256 + wave * 64;
+    const int64_t n0 = (int64_t)blockIdx.x * 256 + wave * 64;
     if (n0 >= p.N) return;
-    const int t0 = blockIdx.x * 16 * SUBS, lg = lane >> 4;
+    const int t0 = blockIdx.z * 16 * SUBS, lg = lane >> 4;
     const int id = lora_id(p, t0, 16 * SUBS, lane);
     const int64_t n = n0 + 16 * lg;  // this lane's 16 columns
     const int left = (int)min(max(p.N - n, (int64_t)0), (int64_t)16);
+    const bool whole = p.vec_cd && left == 16;
     const int chunks = p.ldh / 8;    // of 8 ranks
     auto token = [&](int s) { return t0 + 16 * s + (lane & 15); };
-    // what does not depend on the ids is asked for before they are there
-    float y0[16];
-    u32x4 hv0[PARTS];
-    float down0 = 1.0f;
-    if constexpr (SUBS == 1) {
-        const int t = min(token(0), p.T - 1);
-        if (p.C) lora_load16<OUT>(p.C, (int64_t)t * p.ldc + n, left, p.vec_cd, y0);
-    }
-    lora_groups(id, blockIdx.y, gridDim.y, !p.in_place, [&](const LoraGroup &g) {
+    u32x4 cv[SUBS][CW];
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+        if (p.C && whole && token(s) < p.T) {
+            const u32x4 *c = reinterpret_cast<const u32x4 *>(p.C + ((int64_t)token(s) * p.ldc + n) * OSZ);
+#pragma unroll
+            for (int q = 0; q < CW; ++q) cv[s][q] = c[q];
+        }
+    lora_groups(id, 0, 1, !p.in_place, [&](const LoraGroup &g) {
         const int rank = g.adapter < 0 ? 0 : lora_rank(p, g.adapter);
         const float scale = rank > 0 && p.scales ? p.scales[g.adapter] : 1.0f;
-        f32x4 acc[SUBS][4];
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[s][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        float up = 1.0f;
-        const bool in0 = g.members >> (lane & 15) & 1;
-        if constexpr (SUBS == 1 && IT == IT_F16) {
-            if (rank > 0) {
-                float m = 0.0f;
-                if (in0)
-                    for (int c = lg; c < chunks; c += 4) {
-                        float v[8];
-                        lora_load_h(p, token(0), c, v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
-                    }
-                m = fmaxf(m, __shfl_xor(m, 16));
-                m = fmaxf(m, __shfl_xor(m, 32));
-                const int by = lora_exponent(m);
-                up = lora_pow2(by);
-                down0 = lora_pow2(-by);
-            }
-        }
         const uint8_t *b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t col = n0 + 16 * ((lane & 15) >> 2) + 4 * j + (lane & 3);
             b[j] = p.B + ((int64_t)max(g.adapter, 0) * p.N + (col < p.N ? col : p.N - 1)) * p.ldb * 2;
         }
-        for (int r0 = 0; r0 < rank; r0 += 32 * RS) {
-            u32x4 bv[RS][4];
+        u32x4 bv[RS][4];
+        auto load_b = [&](int r0) {
 #pragma unroll
             for (int q = 0; q < RS; ++q)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) bv[q][j] = stream_chunk<2, VEC>(b[j], r0 + 32 * q + 8 * lg, rank);
+        };
+        if (rank > 0) load_b(0);
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                if (!(g.members >> (16 * s) & 0xffff)) continue;
-                const bool in = g.members >> (16 * s + (lane & 15)) & 1;
+        for (int s = 0; s < SUBS; ++s) {
+            if (!(g.members >> (16 * s) & 0xffff)) continue;
+            const bool in = g.members >> (16 * s + (lane & 15)) & 1;
+            f32x4 acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r0 = 0; r0 < rank; r0 += 32 * RS) {
+                if (rank > 32 * RS) load_b(r0);
+                u32x4 hv[RS][PARTS];
 #pragma unroll
                 for (int q = 0; q < RS; ++q) {
                     const int c = r0 / 8 + 4 * q + lg;
-                    const bool used = in && c < chunks;
-                    if constexpr (SUBS == 1) {
-                        float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                        if (used) lora_load_h(p, token(s), c, v);
-                        lora_split<IT, PARTS>(v, up, hv0);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < PARTS; ++k) {
-                            hv0[k] = u32x4{0u, 0u, 0u, 0u};
-                            if (used)
-                                hv0[k] = *reinterpret_cast<const u32x4 *>(
-                                    p.parts + ((int64_t)k * p.T + token(s)) * p.ldh + 8 * c);
-                        }
+                    for (int k = 0; k < PARTS; ++k) {
+                        hv[q][k] = u32x4{0u, 0u, 0u, 0u};
+                        if (in && c < chunks)
+                            hv[q][k] = *reinterpret_cast<const u32x4 *>(
+                                p.parts + ((int64_t)k * p.T + token(s)) * p.ldh + 8 * c);
                     }
+                }
+#pragma unroll
+                for (int q = 0; q < RS; ++q)
 #pragma unroll
                     for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[s][j] = mfma16_1<IT>(bv[q][j], hv0[k], acc[s][j]);
-                }
+                        for (int j = 0; j < 4; ++j) acc[j] = mfma16_1<IT>(bv[q][j], hv[q][k], acc[j]);
             }
-        }
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) {
-            if (!(g.members >> (16 * s + (lane & 15)) & 1) || left == 0) continue;
+            if (!in || left == 0) continue;
             const int64_t t = token(s);
-            float y[16], by = 1.0f;
-            if constexpr (SUBS == 1) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = y0[e];
-                by = down0;
-            } else {
-                if (p.C) lora_load16<OUT>(p.C, t * p.ldc + n, left, p.vec_cd, y);
-                if (IT == IT_F16 && rank > 0) by = p.down[t];
-            }
+            const float down = IT == IT_F16 && rank > 0 ? p.down[t] : 1.0f;
+            float y[16];
             if (!p.C) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = 0.0f;
+            } else if (whole) {
+                lora_values<OUT>(cv[s], y);
+            } else {
+                lora_load_some<OUT>(p.C, t * p.ldc + n, left, y);
             }
             if (rank > 0) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float v = acc[s][e / 4][e % 4];
-                    y[e] += scale * (IT == IT_F16 ? v * by : v);
+                    const float v = acc[e / 4][e % 4];
+                    y[e] += scale * (IT == IT_F16 ? v * down : v);
                 }
             }
             lora_store16<OUT>(p.D, t * p.ldd + n, left, p.vec_cd, y);

@@ -6,16 +6,17 @@
 
 namespace libgemm {
 
-template <int IT, int OUT, int SUBS, bool VEC>
-const void *lora_up_of(int rank) {
-    return rank <= 32 ? (const void *)lora_up_kernel<IT, OUT, SUBS, 1, VEC>
-                      : (const void *)lora_up_kernel<IT, OUT, SUBS, 2, VEC>;
+template <int IT, int OUT, bool VEC>
+const void *lora_up_of(bool few, int rank) {
+    if (few) return (const void *)lora_up_few_kernel<IT, OUT, VEC>;
+    return rank <= 32 ? (const void *)lora_up_kernel<IT, OUT, 1, VEC>
+                      : (const void *)lora_up_kernel<IT, OUT, 2, VEC>;
 }
-template <int IT, int SUBS, bool VEC>
-const void *lora_up_of(int out_dtype, int rank) {
-    return out_dtype == DT_F32   ? lora_up_of<IT, DT_F32, SUBS, VEC>(rank)
-           : out_dtype == DT_F16 ? lora_up_of<IT, DT_F16, SUBS, VEC>(rank)
-                                 : lora_up_of<IT, DT_BF16, SUBS, VEC>(rank);
+template <int IT, bool VEC>
+const void *lora_up_of(bool few, int out_dtype, int rank) {
+    return out_dtype == DT_F32   ? lora_up_of<IT, DT_F32, VEC>(few, rank)
+           : out_dtype == DT_F16 ? lora_up_of<IT, DT_F16, VEC>(few, rank)
+                                 : lora_up_of<IT, DT_BF16, VEC>(few, rank);
 }
 template <int IT, int RT>
 const void *lora_down_of(bool vec) {
@@ -48,21 +49,20 @@ hipError_t launch_lora(const LoraParams &p, int out_dtype, bool few, bool vec_xa
         e = hipLaunchKernel(k, dim3(tiles64, chunks, (unsigned)p.splits), dim3(256), args, 0, s);
     }
     if (e != hipSuccess) return e;
-    const dim3 grid(few ? tiles16 : tiles64, groups, (unsigned)cdiv(p.N, 256));
-    if (few) {
-        const void *k = vec_b ? lora_up_of<IT, 1, true>(out_dtype, p.rank)
-                              : lora_up_of<IT, 1, false>(out_dtype, p.rank);
-        return hipLaunchKernel(k, grid, dim3(256), args, 0, s);
+    if (!few) {
+        int lanes = 1;  // threads of a token, 8 ranks each
+        while (8 * lanes < p.ldh) lanes *= 2;
+        void *with_lanes[] = {&arg, &lanes};
+        const void *k = out_dtype == DT_F32 ? (const void *)lora_parts_kernel<IT, 3>
+                                            : (const void *)lora_parts_kernel<IT, 2>;
+        e = hipLaunchKernel(k, dim3((unsigned)cdiv(p.T, 256 / lanes)), dim3(256), with_lanes, 0, s);
+        if (e != hipSuccess) return e;
     }
-    int lanes = 1;  // threads of a token, 8 ranks each
-    while (8 * lanes < p.ldh) lanes *= 2;
-    void *with_lanes[] = {&arg, &lanes};
-    const void *k = out_dtype == DT_F32 ? (const void *)lora_parts_kernel<IT, 3>
-                                        : (const void *)lora_parts_kernel<IT, 2>;
-    e = hipLaunchKernel(k, dim3((unsigned)cdiv(p.T, 256 / lanes)), dim3(256), with_lanes, 0, s);
-    if (e != hipSuccess) return e;
-    k = vec_b ? lora_up_of<IT, 4, true>(out_dtype, p.rank) : lora_up_of<IT, 4, false>(out_dtype, p.rank);
-    return hipLaunchKernel(k, grid, dim3(256), args, 0, s);
+    const void *k = vec_b ? lora_up_of<IT, true>(few, out_dtype, p.rank)
+                          : lora_up_of<IT, false>(few, out_dtype, p.rank);
+    const unsigned columns = (unsigned)cdiv(p.N, 256);
+    return hipLaunchKernel(k, few ? dim3(columns, (unsigned)p.T) : dim3(columns, 1, tiles64), dim3(256),
+                           args, 0, s);
 }
 
 hipError_t launch_lora_f16(const LoraParams &, int out_dtype, bool few, bool vec_xa, bool vec_b, hipStream_t);

@@ -50,17 +50,27 @@ __device__ __forceinline__ float balance_exp(float x) {
     return __builtin_isinf(h) ? y : __builtin_fmaf(y, l * 0.69314718f, y);
 }
 
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int s = 1; s < G; s *= 2) v = fmaxf(v, __shfl_xor(v, s));
-    return v;
+// Lane l reads lane l ^ X of its row of 16 (X = 1, 2), its mirror in the half row (which
+// holds the other quad's result) or in the row (the other half's); past rows, LDS exchanges.
+template <int STEP>
+__device__ __forceinline__ float group_other(float v) {
+    if constexpr (STEP <= 8) {
+        constexpr int ctrl = STEP == 1 ? 0xb1 : STEP == 2 ? 0x4e : STEP == 4 ? 0x141 : 0x140;
+        return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), ctrl, 0xf, 0xf, true));
+    } else {
+        return __shfl_xor(v, STEP);
+    }
 }
-template <int G>
+// Over the lanes of a group, the same in all of them.
+template <int G, int STEP = 1>
+__device__ __forceinline__ float group_max(float v) {
+    if constexpr (STEP < G) return group_max<G, 2 * STEP>(fmaxf(v, group_other<STEP>(v)));
+    else return v;
+}
+template <int G, int STEP = 1>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int s = 1; s < G; s *= 2) v += __shfl_xor(v, s);
-    return v;
+    if constexpr (STEP < G) return group_sum<G, 2 * STEP>(v + group_other<STEP>(v));
+    else return v;
 }
 
 // V logits from expert e0 on; experts past E are -Inf.
