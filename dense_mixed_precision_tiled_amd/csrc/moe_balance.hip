@@ -5,20 +5,22 @@
 //   loss = balance E sum_e f_e mean_t(p_te) + z mean_t(lse_t^2)
 //   dl_te = g/n p_te (balance E (f_e - sum_j f_j p_tj) + 2 z lse_t)
 //
-// A group of G lanes takes a token, V experts each (V consecutive ones for a lane: 16-byte
-// loads), so that a row is read once and stays in registers: its maximum is the first
-// round of the selection, the others take the largest value left.  Sums over tokens stay
-// in registers over a thread's tokens; then the groups of a wave, the waves of a workgroup
+// A group of G lanes takes a token, V experts each (consecutive ones for a lane: 16-byte
+// loads), so that a row is read once and stays in registers.  Sums over tokens stay in
+// registers over a thread's tokens; then the groups of a wave, the waves of a workgroup
 // and, in the second kernel, the workgroups are added up in a fixed order.
 //
 // In the gradient f is the same for every token and stays in registers.
+//
+// The first kernel is bound by its vector instructions (the choice of eight experts takes
+// about 120 for a token's lanes), the gradient by memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "../../include/libgemm.h"
 #include "gemm_host.hpp"
-#include "gemm_kernels.hpp"
 #include "gemm_validate.hpp"
+#include "moe.hpp"
 
 namespace libgemm {
 
@@ -63,14 +65,100 @@ __device__ __forceinline__ float group_other(float v) {
 }
 // Over the lanes of a group, the same in all of them.
 template <int G, int STEP = 1>
-__device__ __forceinline__ float group_max(float v) {
-    if constexpr (STEP < G) return group_max<G, 2 * STEP>(fmaxf(v, group_other<STEP>(v)));
-    else return v;
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (STEP < G) {
+        const uint32_t o = __float_as_uint(group_other<STEP>(__uint_as_float(v)));
+        return group_max<G, 2 * STEP>(max(v, o));
+    } else {
+        return v;
+    }
 }
 template <int G, int STEP = 1>
 __device__ __forceinline__ float group_sum(float v) {
     if constexpr (STEP < G) return group_sum<G, 2 * STEP>(v + group_other<STEP>(v));
     else return v;
+}
+
+// The topk largest of a group's keys (moe_key; ties to the lower expert, none at -Inf or
+// NaN): adds 1 to csum of each of a lane's V experts among them.  Returns the largest key.
+//
+// A lane's keys are sorted, four at a time, so that a round looks at one key of each lane
+// (of each four): the group's largest, whose lane's others move up.  Rounds know no ties; where
+// two equal keys go in one round, or there are fewer than topk above -Inf, the keys that are
+// not below the last round's do not number topk, which is counted, and the choice is made
+// again with a round for each single key.
+template <int G, int V>
+__device__ __forceinline__ uint32_t balance_choose(const uint32_t (&key)[V], int topk, uint64_t below,
+                                                   int (&csum)[V]) {
+    constexpr int Q = V / 4;
+    uint32_t x[Q][4];  // descending
+    auto order = [](uint32_t &a, uint32_t &b) {
+        const uint32_t hi = max(a, b);
+        b = min(a, b);
+        a = hi;
+    };
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        uint32_t(&y)[4] = x[q];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = key[4 * q + i];
+        order(y[0], y[1]);
+        order(y[2], y[3]);
+        order(y[0], y[2]);
+        order(y[1], y[3]);
+        order(y[1], y[2]);
+    }
+    uint32_t top = 0, m = 0;
+    for (int r = 0; r < topk; ++r) {
+        m = x[0][0];
+#pragma unroll
+        for (int q = 1; q < Q; ++q) m = max(m, x[q][0]);
+        m = group_max<G>(m);
+        if (r == 0) top = m;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            uint32_t(&y)[4] = x[q];
+            const bool take = y[0] == m;
+            y[0] = take ? y[1] : y[0];
+            y[1] = take ? y[2] : y[1];
+            y[2] = take ? y[3] : y[2];
+            y[3] = take ? 0u : y[3];
+        }
+    }
+    const bool full = m > kMoeNone;  // topk keys above -Inf; or else none at all
+    int chosen = 0;                  // of the wave
+#pragma unroll
+    for (int i = 0; i < V; ++i) chosen += (int)__popcll(__ballot(full && key[i] >= m));
+    const bool plain = chosen * G == topk * (int)__popcll(__ballot(full)) && __ballot(!full && top > kMoeNone) == 0;
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) csum[i] += full && key[i] >= m ? 1 : 0;
+        return top;
+    }
+    uint32_t left[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) left[i] = key[i];
+#pragma unroll 1
+    for (int r = 0; r < topk; ++r) {
+        uint32_t k = left[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) k = max(k, left[i]);
+        k = group_max<G>(k);
+        bool mine = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) mine |= left[i] == k;
+        // the group's first lane that holds it, whose experts are lower, and its first value
+        const uint64_t has = __ballot(mine);
+        bool take = mine && (has & below) == 0 && k > kMoeNone;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool here = take && left[i] == k;
+            csum[i] += here ? 1 : 0;
+            left[i] = here ? 0u : left[i];
+            take = take && !here;
+        }
+    }
+    return top;
 }
 
 // V logits from expert e0 on; experts past E are -Inf.
@@ -92,7 +180,7 @@ __device__ __forceinline__ void balance_load(const float *row, int e0, int E, fl
 }
 
 template <int G, int V, bool VEC>
-__global__ void __launch_bounds__(1024) balance_kernel(BalanceParams p) {
+__global__ void __launch_bounds__(V > 4 ? 256 : 1024) balance_kernel(BalanceParams p) {
     const float none = -__builtin_inff();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int in_group = lane % G, e0 = in_group * V;
@@ -104,58 +192,48 @@ __global__ void __launch_bounds__(1024) balance_kernel(BalanceParams p) {
     int csum[V], live_count = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) psum[i] = 0.0, csum[i] = 0;
-    for (int64_t t = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G; t < p.T; t += step) {
-        const bool masked = p.mask && p.mask[t] == 0;
-        float l[V], left[V];
-        if (masked) {
+    int64_t t = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
+    while (t < p.T) {
+        // 32 tokens in fp32, then on to fp64 (whose conversions take four times as long)
+        float part[V], zpart = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) l[i] = none;
-        } else {
-            balance_load<V, VEC>(p.logits + t * p.ldl, e0, p.E, l);
-        }
-        // NaN is never chosen
+        for (int i = 0; i < V; ++i) part[i] = 0.0f;
+        for (int k = 0; k < 32 && t < p.T; ++k, t += step) {
+            const bool masked = p.mask && p.mask[t] == 0;
+            float l[V];
+            uint32_t key[V];
+            if (masked) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) left[i] = l[i] == l[i] ? l[i] : none;
-        float top = none;
-        for (int r = 0; r < p.topk; ++r) {
-            float m = left[0];
+                for (int i = 0; i < V; ++i) l[i] = none;
+            } else {
+                balance_load<V, VEC>(p.logits + t * p.ldl, e0, p.E, l);
+            }
 #pragma unroll
-            for (int i = 1; i < V; ++i) m = fmaxf(m, left[i]);
-            m = group_max<G>(m);
-            if (r == 0) top = m;
-            // the lowest expert that holds it: the group's first lane, its first value
-            bool mine = false;
-#pragma unroll
-            for (int i = 0; i < V; ++i) mine |= left[i] == m;
-            const uint64_t has = __ballot(mine);
-            bool take = mine && (has & below) == 0 && m > none;
+            for (int i = 0; i < V; ++i) key[i] = moe_key(l[i]);
+            const uint32_t m = balance_choose<G, V>(key, p.topk, below, csum);
+            // (the largest logit's value, 0 where there is none above -Inf)
+            const float top = m > kMoeNone ? __uint_as_float(m >> 31 ? m & 0x7fffffffu : ~m) : 0.0f;
+            float e[V], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const bool here = take && left[i] == m;
-                csum[i] += here ? 1 : 0;
-                left[i] = here ? none : left[i];
-                take = take && !here;
+                e[i] = __expf(l[i] - top);
+                sum += e[i];
             }
-        }
-        const float shift = top > none ? top : 0.0f;
-        float e[V], sum = 0.0f;
+            sum = group_sum<G>(sum);
+            const bool live = !masked && sum != 0.0f;  // (NaN counts)
+            const float lse = masked ? 0.0f : (sum == 0.0f ? none : __logf(sum) + top);
+            const float inv = __builtin_amdgcn_rcpf(sum);
+            if (live) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            e[i] = balance_exp(l[i] - shift);
-            sum += e[i];
+                for (int i = 0; i < V; ++i) part[i] = __builtin_fmaf(e[i], inv, part[i]);
+                zpart = __builtin_fmaf(lse, lse, zpart);
+                ++live_count;
+            }
+            if (in_group == 0) p.lse[t] = lse;
         }
-        sum = group_sum<G>(sum);
-        const bool live = !masked && sum != 0.0f;  // (NaN counts)
-        const float lse = masked ? 0.0f : (sum == 0.0f ? none : logf(sum) + shift);
-        const float inv = 1.0f / sum;
-        if (live) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) psum[i] += (double)(e[i] * inv);
-        }
-        if (in_group == 0) {
-            p.lse[t] = lse;
-            if (live) zsum += (double)lse * (double)lse, ++live_count;
-        }
+        for (int i = 0; i < V; ++i) psum[i] += (double)part[i];
+        zsum += (double)zpart;
     }
     // the groups of the wave
 #pragma unroll
@@ -194,37 +272,60 @@ __global__ void __launch_bounds__(1024) balance_kernel(BalanceParams p) {
     }
 }
 
-// One workgroup of 16 waves: a wave adds up the parts of an expert.
+// Sum over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ double row_sum(double v) {
+    auto other = [](double x, auto ctrl) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const int lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)b, decltype(ctrl)::value, 0xf, 0xf, true);
+        const int hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), decltype(ctrl)::value, 0xf, 0xf, true);
+        return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+    };
+    v += other(v, std::integral_constant<int, 0xb1>{});   // lane ^ 1
+    v += other(v, std::integral_constant<int, 0x4e>{});   // lane ^ 2
+    v += other(v, std::integral_constant<int, 0x141>{});  // the other quad of the half row
+    return v + other(v, std::integral_constant<int, 0x140>{});
+}
+
+// One workgroup: 16 lanes add up the parts (256 at most) of an expert, all of their loads
+// on their way together.  (Counts as doubles, which hold them exactly.)
 __global__ void __launch_bounds__(1024) balance_join_kernel(BalanceParams p) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __shared__ double terms[16], zsum;
-    __shared__ int live;
+    const int lane = threadIdx.x & 15, rows = blockDim.x / 16;
+    __shared__ double terms[64], zsum, live;
     double term = 0.0;
-    for (int e = wave; e <= p.E; e += 16) {
-        double s = 0.0;
-        int c = 0;
-        for (int i = lane; i < p.parts; i += 64)
-            s += p.psum[(int64_t)e * p.parts + i], c += p.csum[(int64_t)e * p.parts + i];
+    for (int e = threadIdx.x / 16; e <= p.E; e += rows) {
+        double s[16];
+        int c[16];
 #pragma unroll
-        for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o), c += __shfl_xor(c, o);
-        if (e < p.E) term += s * (double)c;
+        for (int i = 0; i < 16; ++i) {
+            const int64_t at = (int64_t)e * p.parts + min(lane + 16 * i, p.parts - 1);
+            s[i] = p.psum[at];
+            c[i] = p.csum[at];
+        }
+        double sum = 0.0, count = 0.0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (lane + 16 * i < p.parts) sum += s[i], count += (double)c[i];
+        sum = row_sum(sum);
+        count = row_sum(count);
+        if (e < p.E) term += sum * count;
         if (lane == 0) {
-            p.counts[e] = c;
-            if (e == p.E) zsum = s, live = c;
+            p.counts[e] = (int)count;
+            if (e == p.E) zsum = sum, live = count;
         }
     }
-    if (lane == 0) terms[wave] = term;
+    if (lane == 0) terms[threadIdx.x / 16] = term;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int w = 0; w < 16; ++w) s += terms[w];
-        const double n = (double)live;
-        const double b = live ? (double)p.E * s / (n * n * (double)p.topk) : 0.0;
-        const double z = live ? zsum / n : 0.0;
-        p.loss[0] = (float)((double)p.balance * b + (double)p.z * z);
-        p.loss[1] = (float)b;
-        p.loss[2] = (float)z;
-    }
+    if (threadIdx.x >= 16) return;
+    double s = 0.0;
+    for (int i = lane; i < rows; i += 16) s += terms[i];
+    s = row_sum(s);
+    if (lane != 0) return;
+    const double n = live;
+    const double b = n > 0.0 ? (double)p.E * s / (n * n * (double)p.topk) : 0.0;
+    const double z = n > 0.0 ? zsum / n : 0.0;
+    p.loss[0] = (float)((double)p.balance * b + (double)p.z * z);
+    p.loss[1] = (float)b;
+    p.loss[2] = (float)z;
 }
 
 template <int G, int V, int OUT, bool VEC>
@@ -377,7 +478,8 @@ int gemm_moe_balance(int64_t T, int64_t E, int64_t topk, const float *logits, in
         return hipLaunchKernel(k, dim3((unsigned)p.parts), dim3(threads), args, lds, s);
     });
     if (e == hipSuccess)
-        e = hipLaunchKernel((const void *)balance_join_kernel, dim3(1), dim3(1024), args, 0, s);
+        e = hipLaunchKernel((const void *)balance_join_kernel, dim3(1),
+                            dim3(E < 16 ? 256 : E < 32 ? 512 : 1024), args, 0, s);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 

@@ -6,7 +6,7 @@ l - lse) of size a is rounded to a e, its evaluation adds at most 4 e relatively
 E experts adds (E + 2) e, so p is off by d = (2 a + E + 16) e relatively, with a the
 spread of the token's logits (for the gradient also |lse| e from lse's rounding).  lse is
 off by d + 4 e |lse|, from the logarithm and the addition of the maximum.  Sums over tokens
-are fp64.  f is off by 3 e; the gradient's bracket adds a few products:
+are fp32 over 32 of them (32 e of the sum) and fp64 beyond.  f is off by 3 e; the gradient's bracket adds a few products:
 |g| p (balance E (|f| + sum f p) (2 d + 8 e) + 2 z (|lse| (d + 8 e) + d)), rounded once.
 A p below 2^-126, fp32's smallest normal value, may be 0 (the exponential's result is not
 kept as a subnormal), and products below that lose bits: twice 2^-126 of everything p is
@@ -100,8 +100,8 @@ class Balance:
         assert (np.abs(gs.double().numpy()[~same] - lse[~same]) <= dl[~same]).all()
         n = max(counts[-1], 1)
         f = counts[:-1] / (n * self.topk)
-        db = self.E * (f * (p * rel).sum(0)).sum() / n + 2 * e24 * loss[1]
-        dz = (2 * flse * dl + dl ** 2).sum() / n + 2 * e24 * loss[2]
+        db = self.E * (f * (p * rel).sum(0)).sum() / n + 34 * e24 * loss[1]
+        dz = (2 * flse * dl + dl ** 2).sum() / n + 34 * e24 * loss[2]
         got = gl.double().numpy()
         bound = [abs(b32) * db + abs(z32) * dz + 2 * e24 * (abs(b32) * loss[1] + abs(z32) * loss[2]), db, dz]
         for v, want, b in zip(got, loss, bound):
