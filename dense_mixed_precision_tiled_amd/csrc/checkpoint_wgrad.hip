@@ -24,12 +24,12 @@ namespace libgemm {
 // element-wise loads.  128 x 128 tiles of D, four waves, 64 tokens at a time.
 constexpr int kWgAnyBM = 128, kWgAnyBN = 128;
 
-template <int IT>
+template <int IT, int OUT>
 __global__ void __launch_bounds__(256) wgrad_any_kernel(WgradParams p) {
     using CF = TileCfg<kWgAnyBM, kWgAnyBN, 64, 2, 2, 32>;
     constexpr int BK = 64, CA = CF::BM / 8, CB = CF::BN / 8, TM = CF::TM, TN = CF::TN;
     constexpr int NA = BK * CA / 256, NB = BK * (CF::BN / 16) / 256;
-    __shared__ u32x4 smem[BK * (CA + CB) + 512];
+    __shared__ u32x4 smem[BK * (CA + CB)];
     u32x4 *const sA = smem, *const sB = smem + BK * CA;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
@@ -109,11 +109,8 @@ __global__ void __launch_bounds__(256) wgrad_any_kernel(WgradParams p) {
                 for (int j = 0; j < TN; ++j) acc[i][j] = mfma32_1<IT>(fb[j], fa[i], acc[i][j]);
         }
     }
-    __syncthreads();
-    if (p.g.splits > 1)
-        wgrad_store_part<CF>(p.g, acc, n0, k0, tid);
-    else
-        tile_epilogue<CF, IT, true, (BK * (CA + CB) + 512) * 16>(p.g, acc, n0, k0, smem, tid);
+    if constexpr (OUT < 0) wgrad_store_part<CF>(p.g, acc, n0, k0, tid);
+    else wgrad_store<CF, OUT>(p.g, acc, n0, k0, tid);
 }
 
 // D = the parts' sums + C: four columns of a row for each thread.
@@ -145,19 +142,23 @@ using namespace libgemm_host;
 
 namespace {
 
-// Inputs' type, tile -> kernel.
-template <int IT>
-const void *tile_kernel(const WgradPlan &plan, unsigned *threads) {
-    if (plan.bm == 256) {
-        *threads = CfgLarge8::THREADS;
-        return (const void *)wgrad_tile_kernel<CfgLarge8, IT>;
-    }
-    if (plan.bm == 128) {
-        *threads = CfgMedium::THREADS;
-        return (const void *)wgrad_tile_kernel<CfgMedium, IT>;
-    }
-    *threads = 64 * kThinWaves;
+// Inputs' type, D's type (or a part's sums), tile -> kernel.
+template <int IT, int OUT>
+const void *wgrad_of(const WgradPlan &plan, bool vec, unsigned *threads) {
+    *threads = 256;
+    if (!vec) return (const void *)wgrad_any_kernel<IT, OUT>;
+    if (plan.bm == 128) return (const void *)wgrad_tile_kernel<CfgMedium, IT, OUT>;
+    *threads = 512;
+    static_assert(CfgMedium::THREADS == 256 && CfgLarge8::THREADS == 512 && 64 * kThinWaves == 512, "threads");
+    if (plan.bm == 256) return (const void *)wgrad_tile_kernel<CfgLarge8, IT, OUT>;
     return plan.bm == 32 ? (const void *)wgrad_thin_kernel<IT, 1> : (const void *)wgrad_thin_kernel<IT, 2>;
+}
+template <int IT>
+const void *wgrad_of(const WgradPlan &plan, bool vec, int out_dtype, unsigned *threads) {
+    if (plan.splits > 1) return wgrad_of<IT, -1>(plan, vec, threads);
+    return out_dtype == GEMM_F32   ? wgrad_of<IT, DT_F32>(plan, vec, threads)
+           : out_dtype == GEMM_F16 ? wgrad_of<IT, DT_F16>(plan, vec, threads)
+                                   : wgrad_of<IT, DT_BF16>(plan, vec, threads);
 }
 
 template <int OUT>
@@ -216,12 +217,10 @@ int gemm_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_
         g.ws = reinterpret_cast<float *>(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
     p.ldq = ldq;
     p.lds = lds;
-    const bool bf16 = in_dtype == GEMM_BF16;
     hipStream_t s = static_cast<hipStream_t>(stream);
     unsigned threads = 256;
-    const void *k;
-    if (!vec) k = bf16 ? (const void *)wgrad_any_kernel<IT_BF16> : (const void *)wgrad_any_kernel<IT_F16>;
-    else k = bf16 ? tile_kernel<IT_BF16>(plan, &threads) : tile_kernel<IT_F16>(plan, &threads);
+    const void *k = in_dtype == GEMM_BF16 ? wgrad_of<IT_BF16>(plan, vec, out_dtype, &threads)
+                                          : wgrad_of<IT_F16>(plan, vec, out_dtype, &threads);
     // a grid holds fewer than 2^32 threads: at most 2^27 rows and columns of D for each launch
     const int64_t most = (int64_t)1 << 27;
     for (int64_t i = 0; i < N; i += most) {

@@ -438,12 +438,14 @@ inline int validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int
 // Up to 64 outputs the thin kernel (bm 32, 64) streams Q: parts of at least 256 tokens
 // while there is less than a workgroup for each CU (16 x 4096 of 8192 tokens, us of the
 // kernel and the join: 8 parts 15.0, 4 18.1, 16 18.5).  Past that, the tile and the number
-// of parts with the least modelled time, in us: a workgroup's start and end, a step of 64
-// tokens (128 x 128: 0.75 alone on the GPU, 1.05 on every CU, 1.65 with two on each;
-// 256 x 256: 1.85), and the parts' sums written and read.  Measured against the model:
-// 1001 x 2056 of 3999 256 in 6 parts 51.1 (59), 128 in 3 52.8 (58), 128 in 1 69 (67);
-// 512 x 512 of 8192 128 in 12 31.0 (29), 256 in 24 33.1 (37); 4096 x 4096 of 512 256 40.0
-// (41), 128 46.9 (43).
+// of parts with the least modelled time, in us: a workgroup's start and end (128 x 128: 5.9,
+// 256 x 256: 8.2), its steps of 64 tokens (128: 0.73 alone on the GPU, 0.83 on every CU, 1.18
+// with two on each; 256: 1.34 to 1.6), and the parts' sums written and read.  The constants
+// are fitted to 290 measured (shape, tile, parts) of 24 shapes, 7% off in the mean, and the
+// plan takes 0.8% longer than the best measured one.  Measured (best of the other tile
+// beside it): 1001 x 2056 of 3999 128 in 3 40.4 (256 in 6 41.2; 128 whole 55); 512 x 512 of
+// 8192 128 in 16 19.9 (26.8); 4096 x 4096 of 4096 256 134.7 (184); 1024 x 4096 of 2048 128
+// whole 36.8 (43.6; 128 in 2 41.1); 2048 x 2048 of 4096 128 in 2 59.1 (256 in 3 58.6).
 struct WgradPlan {
     int64_t bm, bn, splits, per;  // per: tokens of a part, a multiple of 64
 };
@@ -466,10 +468,11 @@ inline WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
                  ++i) {
                 const double groups = tiles * i, per = (double)((steps + i - 1) / i);
                 const auto rounds = [&](double at_once) { return (double)(int64_t)((groups + at_once - 1) / at_once); };
-                double t = tile == 256    ? 14 + per * 1.85 * rounds(256)
-                           : groups <= 256 ? 10 + per * (0.75 + 0.3 * groups / 256)
-                                           : 10 + per * 1.65 * rounds(512);
-                if (i > 1) t += 3 + (double)i * (double)N * (double)K * 8 / 4.5e6;
+                const double busy = groups < 256 ? groups / 256 : 1;
+                double t = tile == 256    ? 8.2 + per * (1.34 + 0.26 * busy) * rounds(256)
+                           : groups <= 256 ? 5.9 + per * (0.73 + 0.1 * busy)
+                                           : 5.9 + per * 1.18 * (0.6 * rounds(512) + 0.4 * groups / 512);
+                if (i > 1) t += 2.1 + (double)i * (double)N * (double)K * 8 / 6e6;
                 if (best == 0 || t < best) best = t, w.bm = w.bn = tile, s = i;
             }
         }

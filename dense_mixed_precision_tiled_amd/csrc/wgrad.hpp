@@ -318,7 +318,51 @@ __device__ __forceinline__ void wgrad_store_part(const Params &p, const f32x16 (
     });
 }
 
-template <class CF, int IT>
+// D's rows straight from the accumulators, four columns for each store, one rounding.  All of
+// C is added to the accumulators before the first store: a wait for a load waits for every
+// store issued before it.  (tile_epilogue, which can do more, takes 5 us more for a tile of
+// 128 x 128.)
+template <class CF, int OUT>
+__device__ __forceinline__ void wgrad_store(const Params &p, f32x16 (&acc)[CF::TM][CF::TN],
+                                            int m0, int n0, int tid) {
+    const int lane = tid & 63, wave = tid >> 6;
+    constexpr int NG = CF::TN * 4;
+    using Raw = typename std::conditional<OUT == DT_F32, u32x4, u32x2>::type;
+    const int row0 = m0 + wave / CF::WAVES_N * CF::WTM + acc_row<32>(lane);
+    const int col0 = n0 + wave % CF::WAVES_N * CF::WTN + acc_col<32>(lane, 0);
+    auto col_of = [&](int g) { return col0 + 32 * (g / 4) + 8 * (g % 4); };
+    if (p.C && p.cd_vec)
+        Unroll<0, CF::TM>::run([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            const int row = row0 + 32 * i;
+            Raw c[NG];
+            Unroll<0, NG>::run([&](auto gg) {
+                constexpr int g = decltype(gg)::value;
+                c[g] = Raw{};
+                if (row < p.M && col_of(g) + 4 <= p.N) c[g] = load_c_raw<OUT>(p, row, col_of(g));
+            });
+            Unroll<0, NG>::run([&](auto gg) {
+                constexpr int g = decltype(gg)::value, j = g / 4, r = g % 4 * 4;
+                const f32x4 v = c_from_raw<OUT>(c[g]);
+                acc[i][j][r] += v[0], acc[i][j][r + 1] += v[1];
+                acc[i][j][r + 2] += v[2], acc[i][j][r + 3] += v[3];
+            });
+        });
+    Unroll<0, CF::TM>::run([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        const int row = row0 + 32 * i;
+        if (row >= p.M) return;
+        Unroll<0, NG>::run([&](auto gg) {
+            constexpr int g = decltype(gg)::value, j = g / 4, r = g % 4 * 4;
+            const f32x4 v = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+            if (p.cd_vec && col_of(g) + 4 <= p.N) finish4<OUT, true, false, true>(p, row, col_of(g), v);
+            else if (col_of(g) < p.N) finish4<OUT, false, false>(p, row, col_of(g), v);
+        });
+    });
+}
+
+// OUT: the type of D, or less than 0 for the sums of a part.
+template <class CF, int IT, int OUT>
 __global__ void __launch_bounds__(CF::THREADS, 2) wgrad_tile_kernel(WgradParams p) {
     using L = WgradLoop<CF, IT>;
     __shared__ u32x4 smem[L::LDS_BYTES / 16];
@@ -333,12 +377,9 @@ __global__ void __launch_bounds__(CF::THREADS, 2) wgrad_tile_kernel(WgradParams 
         Unroll<0, CF::TN>::run([&](auto j) { acc[decltype(i)::value][decltype(j)::value] = f32x16{}; });
     });
     L(p, reinterpret_cast<char *>(smem), tid, n0, k0, beg, end).run(acc);
-    wait_vmcnt<0>();  // the loads past the last tile have landed
-    __syncthreads();  // everywhere, and no wave reads the stages that the epilogue takes
-    if (p.g.splits > 1)
-        wgrad_store_part<CF>(p.g, acc, n0, k0, tid);
-    else
-        tile_epilogue<CF, IT, true, L::LDS_BYTES>(p.g, acc, n0, k0, smem, tid);
+    if constexpr (OUT < 0) wgrad_store_part<CF>(p.g, acc, n0, k0, tid);
+    else wgrad_store<CF, OUT>(p.g, acc, n0, k0, tid);
+    wait_vmcnt<0>();  // the loads past the last tile land before the workgroup's LDS is released
 }
 
 }  // namespace libgemm
