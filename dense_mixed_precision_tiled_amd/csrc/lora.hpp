@@ -444,6 +444,92 @@ __global__ void __launch_bounds__(256) lora_up_few_kernel(LoraParams p) {
     else reinterpret_cast<uint16_t *>(p.D)[at] = (uint16_t)to_out16<OUT>(y, false);
 }
 
+// A few tokens and small adapters: both products in one launch.  Each workgroup makes the
+// token's h for itself (A comes from the caches after the first), a wave the dot products of
+// ranks wave, wave + 16, ..., whose rows it reads a KiB at a time, and then 256 columns of D,
+// whose part of B it has asked for before.
+// Grid: x blocks of 256 columns, y tokens.
+template <int IT, int OUT, int RT>
+__global__ void __launch_bounds__(1024) lora_one_kernel(LoraParams p) {
+    constexpr int RANKS = 16 * RT, DT = IT == IT_F16 ? DT_F16 : DT_BF16;
+    __shared__ float h[RANKS];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), t = blockIdx.y;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, row = min(n, (int64_t)p.N - 1);
+    const int id = uniform(p.ids[t]);
+    const bool has = id >= 0 && id < p.adapters;
+    if (!has && p.in_place) return;
+    const int rank = has ? lora_rank(p, id) : 0;
+    float c = 0.0f, scale = 1.0f;
+    u32x4 bv[2 * RT];
+    if (wave < 4) {
+        if (rank > 0) {
+            const uint8_t *b = p.B + ((int64_t)id * p.N + row) * p.ldb * 2;
+#pragma unroll
+            for (int q = 0; q < 2 * RT; ++q) bv[q] = stream_chunk<2, true>(b, 8 * q, rank);
+            if (p.scales) scale = p.scales[id];
+        }
+        if (p.C) {
+            const int64_t at = (int64_t)t * p.ldc + row;
+            if constexpr (OUT == DT_F32) c = reinterpret_cast<const float *>(p.C)[at];
+            else c = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p.C)[at]);
+        }
+    }
+    float y = c;
+    if (rank > 0) {
+        const uint8_t *x = p.X + (int64_t)t * p.ldx * 2, *a[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = 16 * i + wave;  // (past the rank: its first, not kept)
+            a[i] = p.A + ((int64_t)id * p.rank + (r < rank ? r : 0)) * p.lda * 2;
+        }
+        float dot[RT][4] = {};
+        auto add = [&](float &to, const u32x4 &u, const u32x4 &v) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                to = __builtin_fmaf(from_out16<DT>(half_of(u, e)), from_out16<DT>(half_of(v, e)), to);
+        };
+        int k = 0;
+        for (; k + 2048 <= p.K; k += 2048) {
+            u32x4 xv[4], av[RT][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t at = (int64_t)(k + 512 * q + 8 * lane) * 2;
+                xv[q] = *reinterpret_cast<const u32x4 *>(x + at);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) av[i][q] = *reinterpret_cast<const u32x4 *>(a[i] + at);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) add(dot[i][q], av[i][q], xv[q]);
+        }
+        for (; k < p.K; k += 512) {
+            const u32x4 xv = stream_chunk<2, true>(x, k + 8 * lane, p.K);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) add(dot[i][0], stream_chunk<2, true>(a[i], k + 8 * lane, p.K), xv);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float sum = (dot[i][0] + dot[i][1]) + (dot[i][2] + dot[i][3]);
+#pragma unroll
+            for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
+            // (a masked term of the second product is 0 * 0, also where h is not finite)
+            if (lane == 0) h[16 * i + wave] = 16 * i + wave < rank ? sum : 0.0f;
+        }
+        __syncthreads();
+        if (wave < 4) {
+            float d = 0.0f;
+#pragma unroll
+            for (int e = 0; e < RANKS; ++e) d = __builtin_fmaf(from_out16<DT>(half_of(bv[e / 8], e % 8)), h[e], d);
+            y = __builtin_fmaf(scale, d, c);
+        }
+    }
+    if (wave >= 4 || n >= p.N) return;
+    const int64_t at = (int64_t)t * p.ldd + n;
+    if constexpr (OUT == DT_F32) reinterpret_cast<float *>(p.D)[at] = y;
+    else reinterpret_cast<uint16_t *>(p.D)[at] = (uint16_t)to_out16<OUT>(y, false);
+}
+
 // Many tokens: D of 64 tokens and an adapter at a time; a wave takes 64 columns.  Its four
 // row tiles interleave the columns by fours, so that a lane ends up with 16 consecutive
 // ones: row i of tile j is column 16 (i / 4) + 4 j + i % 4.

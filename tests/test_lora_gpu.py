@@ -130,6 +130,51 @@ def test_shapes(T, K, N, rank, adapters, i, o, how):
     Lora(T, K, N, rank, adapters, i, o, how, c=(T + N) % 3 != 0, ranks=T % 2 == 0, scales=K % 3 != 0).call().check()
 
 
+# Past what one launch takes (more than 256 blocks of columns, a rank past 32 or a long A),
+# and around it; prompts with long rows, large ranks and every token its own adapter.
+LONGER = [
+    (1, 2048, 256, 16, 2), (3, 2600, 520, 20, 2), (2, 8192, 40, 32, 2), (2, 8200, 40, 32, 2), (2, 16384, 40, 9, 2),
+    (2, 16392, 40, 9, 2), (256, 40, 256, 4, 300), (129, 40, 257, 4, 3), (40, 1100, 2000, 12, 9), (70, 700, 1100, 30, 70),
+    (5, 1200, 300, 128, 4), (290, 2100, 300, 100, 5), (500, 1500, 130, 256, 3), (300, 4100, 70, 33, 280),
+    (321, 1024, 520, 64, 3)]
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("i,o", [(BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("T,K,N,rank,adapters", LONGER)
+def test_longer_shapes(T, K, N, rank, adapters, i, o, how):
+    Lora(T, K, N, rank, adapters, i, o, how, ranks=T % 2 == 0, seed=1).call().check()
+
+
+@pytest.mark.parametrize("T,N", [(16, 1100), (80, 1100), (300, 1100)])
+def test_bad_values_in_place_and_captured(T, N):
+    """The three ways of the kernels: one launch, two, and prompts."""
+    w = Lora(T, 128, N, 16, 4, ids=[t % 5 - 1 for t in range(T)])
+    clean = w.call().dD.get()
+    w.check()
+    w.A[2 * 16 + 3, 7] = float("nan")
+    w.X[1, 5] = float("inf")
+    w.dA.view.copy_(w.A)
+    w.dX.view.copy_(w.X)
+    first = w.call().dD.get()
+    for t in range(T):
+        if t % 5 == 3:
+            assert first[t].isnan().all()
+        elif t == 1:
+            assert not first[t].isfinite().any()
+        else:
+            assert torch.equal(first[t], clean[t])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.call(w.dC)
+    for _ in range(3):
+        w.dC.view.copy_(w.C)
+        graph.replay()
+        assert torch.equal(w.dC.get().view(torch.int16), first.view(torch.int16))
+        w.call()
+
+
 @pytest.mark.parametrize("i", [BF16, F16])
 @pytest.mark.parametrize("T", [40, 257, 1100])
 def test_packed_prompts(T, i):
@@ -213,7 +258,7 @@ def test_fp16_inner_values_of_any_size(size):
 
 def test_fp16_inner_values_past_65504():
     w = Lora(20, 512, 40, 16, 3, F16, F32, c=False)
-    w.X, w.A = torch.full_like(w.X, 200.0), torch.full_like(w.A, 30.0)  # h = 3 072 000
+    w.X, w.A = torch.full_like(w.X, 200.0), torch.full_like(w.A, 30.0)  # h past 3e6
     w.A[::2] = 2.0 ** -14
     w.dX.view.copy_(w.X)
     w.dA.view.copy_(w.A)
