@@ -399,3 +399,69 @@ def test_wgrad_long_offsets():
     ok(lg.gemm_checkpoint_wgrad(M, N, K, dG.data_ptr(), ldg, dQ.data_ptr(), ldq, dS.data_ptr(), S.shape[1], 0, K,
                                 D.data_ptr(), K, BF16, F32, ws.data_ptr(), ws.numel(), stream()))
     assert np.array_equal(D.cpu().double().numpy(), G.T @ X)
+
+
+# Tiles of 256 x 256, whole and in parts, their edges ragged; tiles of 128 in many parts, the
+# last of them with less than 64 tokens; thin ones of several stretches.
+WG_LARGE = [(520, 4100, 4090), (8200, 1530, 1540), (3203, 515, 520), (6410, 70, 300), (9000, 33, 130)]
+
+
+@pytest.mark.parametrize("i,o,add", [(BF16, F32, True), (F16, F16, True), (BF16, BF16, False)])
+@pytest.mark.parametrize("M,N,K", WG_LARGE)
+def test_wgrad_large(M, N, K, i, o, add):
+    w = Wgrad(M, N, K, i, o, add=add).call()
+    w.check()
+    if add:  # and in place, to the same bits
+        first = w.dD.get()
+        w.call(w.dC)
+        assert torch.equal(w.dC.get(), first)
+
+
+@pytest.mark.parametrize("M", [200, 1351])
+@pytest.mark.parametrize("how", ["vec", "odd"])
+def test_wgrad_nan_and_inf_in_tiles(M, how):
+    """Also in the rows that the last step of a tile takes once more."""
+    w = Wgrad(M, 200, 192, BF16, F32, how=how)
+    w.S[M - 20, 1] = w.S[M - 60, 4] = 255  # columns 32 to 63 and 128 to 159
+    w.dS.view.copy_(torch.from_numpy(w.S))
+    w.G[M - 64, 3], w.G[M - 1, 150], w.G[5, 60] = float("inf"), float("nan"), float("-inf")
+    w.dG.view.copy_(w.G)
+    got = w.call().dD.get().numpy()
+    bad = np.zeros((200, 192), bool)
+    bad[:, 32:64] = bad[:, 128:160] = True
+    bad[[3, 150, 60]] = True
+    assert np.array_equal(~np.isfinite(got), bad)
+
+
+@pytest.mark.parametrize("N", [16, 100])
+@pytest.mark.parametrize("wide", [0, 16])
+def test_wgrad_long_lines(N, wide):
+    """Rows of G, Q and S past 4 GiB, at the longest lines of 32-bit offsets and past them."""
+    M, K, ldg, ldq, lds = 140, 96, 1 << 24, (1 << 25) + wide, 1 << 25
+    w = Wgrad(M, N, K, BF16, F32, ints=True)
+
+    def spread(m, ld, dtype):
+        buf = torch.empty((M - 1) * ld + m.shape[1], dtype=dtype, device="cuda")
+        torch.as_strided(buf, tuple(m.shape), (ld, 1)).copy_(m if torch.is_tensor(m) else torch.from_numpy(m))
+        return buf
+
+    G, Q = spread(w.G, ldg, torch.bfloat16), spread(w.Q, ldq, torch.int8)
+    S = spread(w.S, lds, torch.uint8)
+    ok(lg.gemm_checkpoint_wgrad(M, N, K, G.data_ptr(), ldg, Q.data_ptr(), ldq, S.data_ptr(), lds, 0, w.dD.ld,
+                                w.dD.ptr, w.dD.ld, BF16, F32, w.ws.data_ptr() if w.size else 0, w.size, stream()))
+    assert np.array_equal(w.dD.get().double().numpy(), w.reference()[0])
+
+
+def test_wgrad_tiles_captured():
+    w = Wgrad(1500, 200, 300, add=True)
+    assert w.size > 0
+    eager = w.call().dD.get()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.call()
+    for _ in range(3):
+        w.dD.view.zero_()
+        graph.replay()
+        assert torch.equal(w.dD.get(), eager)
+        w.call()
