@@ -324,7 +324,8 @@ inline LoraWorkspace lora_workspace(int64_t T, const gemm_lora_t *l) {
     w.splits = lora_splits(T, l);
     w.ldh = (l->rank + 7) / 8 * 8;
     w.parts = (w.splits * T * w.ldh * 4 + 255) / 256 * 256;
-    w.down = w.parts + (T > kLoraFew ? 3 * T * w.ldh * 2 : 0);
+    // (up to three values, whole 16 tokens by 32 ranks)
+    w.down = w.parts + (T > kLoraFew ? 3 * ((T + 15) / 16 * 16) * ((w.ldh + 31) / 32 * 32) * 2 : 0);
     w.bytes = w.down + (T > kLoraFew ? 4 * T : 0) + 255;
     return w;
 }

@@ -9,19 +9,20 @@
 // Which adapters the tokens of a tile use is found by every wave from their ids: a round
 // of the loop takes the first token left, its adapter and all the tokens that share it.
 // Packed prompts have one round almost everywhere, and a decoding batch one for each
-// request; no sort, no list in memory.  A column of an MFMA holds one token, so nothing of
-// an adapter reaches another's tokens, which take no part in the round's stores.
+// request; no sort, no list in memory.  A row (or column) of an MFMA holds one token, so
+// nothing of an adapter reaches another's tokens, which take no part in the round's stores.
 //
-// Up to kLoraFew tokens (a decoding batch) what counts is latency: two kernels, weights
-// straight from memory to the registers, the first 16 tokens and an adapter for each
-// workgroup, the second a token for each wave.  More tokens (prompts) are taken 64 at a
-// time, and what counts is the data: X and A go through LDS (read in the MFMA's own shape,
-// a lane's 16 bytes are a request of their own, 64 cycles of a CU's address path for each
-// KiB), and a wave keeps B's part in registers for its 64 tokens.
+// Up to kLoraFew tokens (a decoding batch) what counts is latency: weights straight from
+// memory to the registers, for a few tokens in one kernel (lora_one_kernel), for more in two,
+// the first 16 tokens and an adapter for each workgroup, the second a token for each wave.
+// More tokens (prompts) are taken 64 at a time, and what counts is the data: X and A go
+// through LDS (read in the MFMA's own shape, a lane's 16 bytes are a request of their own, 64
+// cycles of a CU's address path for each KiB), and a wave of the second kernel keeps B's part
+// in registers for its 32 tokens.
 //
-// Kernels on 4096 x 4096 in bf16, us: one token, rank 16, 3.7 and 3.5; 64 tokens of 64
-// adapters 5.9 and 4.6 (16.8 MB of weights); 4096 tokens, rank 64, 8 adapters 16.2, 4.8 and
-// 26.9 (2.1 and 2.5 TB/s).
+// Kernels on 4096 x 4096 in bf16, us: one token, rank 16, 4.9; 64 tokens of 64 adapters 5.9
+// and 4.5 (16.8 MB of weights); 4096 tokens, rank 64, 8 adapters 16.2, 4.8 and 28 (2.1 and
+// 2.4 TB/s).
 #pragma once
 
 #include "stream.hpp"
@@ -39,7 +40,7 @@ struct LoraParams {
     int in_place;   // C == D: tokens without an adapter are left alone
     int vec_cd;     // 16-byte accesses to rows of C and D
     float *h;        // [splits][T][ldh]
-    uint16_t *parts; // many tokens: [parts][T][ldh], the values of 16 bits whose sum is h
+    uint16_t *parts; // many tokens: the values of 16 bits whose sum is h, as lora_part() lays them out
     float *down;     // many tokens, fp16: [T], the power of two that the sum is multiplied with
     int ldh, splits, k_per_split;  // k_per_split: a multiple of 128
 };
@@ -47,6 +48,15 @@ struct LoraParams {
 // h is held as two 16-bit values for 16-bit outputs, three for fp32 ones.
 template <int OUT>
 constexpr int kLoraParts = OUT == DT_F32 ? 3 : 2;
+
+// Ranks 8 c .. 8 c + 7 of value q of token t in LoraParams::parts, in chunks of 8: by 16
+// tokens, value and 32 ranks, and there in the order of the MFMA's lanes, so that a wave
+// reads a KiB in a row.  (Read by rows of h, a lane's 16 bytes are a request of their own.)
+template <int PARTS>
+__device__ __forceinline__ int64_t lora_part(const LoraParams &p, int64_t t, int q, int c) {
+    const int wide = (p.ldh + 31) / 32;
+    return (((t / 16) * PARTS + q) * wide + c / 4) * 64 + c % 4 * 16 + t % 16;
+}
 
 // Tokens of a tile that share an adapter.
 struct LoraGroup {
@@ -307,85 +317,73 @@ __device__ __forceinline__ void lora_load_h(const LoraParams &p, int64_t t, int 
     for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
 }
 
-// Many tokens: a thread takes 8 ranks of a token, 32 (or fewer) threads a token.
+// Many tokens: a thread takes 8 ranks of a token (0 past the last, up to a multiple of 32), 32
+// (or fewer) threads a token.
 template <int IT, int PARTS>
 __global__ void __launch_bounds__(256) lora_parts_kernel(LoraParams p, int lanes) {
     const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
     const int c = threadIdx.x % lanes;
     const bool in = t < p.T && 8 * c < p.ldh;
-    float v[8], m = 0.0f, up = 1.0f;
+    float v[8] = {}, m = 0.0f, up = 1.0f;
     // (a token without an adapter has no h: what is there is split, and not used)
     if (in) lora_load_h(p, t, c, v);
     if constexpr (IT == IT_F16) {
-        if (in) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
-        }
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[e]));
         for (int s = 1; s < lanes; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
         const int by = lora_exponent(m);
         up = lora_pow2(by);
         if (in && c == 0) p.down[t] = lora_pow2(-by);
     }
-    if (!in) return;
+    if (t >= p.T || c >= (p.ldh + 31) / 32 * 4) return;
     u32x4 w[PARTS];
     lora_split<IT, PARTS>(v, up, w);
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
-        *reinterpret_cast<u32x4 *>(p.parts + ((int64_t)q * p.T + t) * p.ldh + 8 * c) = w[q];
+        reinterpret_cast<u32x4 *>(p.parts)[lora_part<PARTS>(p, t, q, c)] = w[q];
 }
 
-// 16 values of a row of C or D, as many as n: from 16-byte loads, or one by one.
+// Four values of a row of C or D: from one load, or as many as n.
 template <int OUT>
-__device__ __forceinline__ void lora_values(const u32x4 (&w)[OUT == DT_F32 ? 4 : 2], float (&y)[16]) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        if constexpr (OUT == DT_F32) y[e] = __uint_as_float(w[e / 4][e % 4]);
-        else y[e] = from_out16<OUT>(half_of(w[e / 8], e % 8));
-    }
+using LoraQuad = typename std::conditional<OUT == DT_F32, u32x4, u32x2>::type;
+template <int OUT>
+__device__ __forceinline__ f32x4 lora_values(const LoraQuad<OUT> &w) {
+    if constexpr (OUT == DT_F32)
+        return f32x4{__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3])};
+    else
+        return f32x4{from_out16<OUT>(w[0] & 0xffffu), from_out16<OUT>(w[0] >> 16),
+                     from_out16<OUT>(w[1] & 0xffffu), from_out16<OUT>(w[1] >> 16)};
 }
 template <int OUT>
-__device__ __forceinline__ void lora_load_some(const uint8_t *p, int64_t at, int n, float (&y)[16]) {
+__device__ __forceinline__ f32x4 lora_load_some(__amdgpu_buffer_rsrc_t rows, uint32_t voff, uint32_t soff, int n) {
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        y[e] = 0.0f;
+    for (int e = 0; e < 4; ++e)
         if (e < n) {
-            if constexpr (OUT == DT_F32) y[e] = reinterpret_cast<const float *>(p)[at + e];
-            else y[e] = from_out16<OUT>(reinterpret_cast<const uint16_t *>(p)[at + e]);
+            if constexpr (OUT == DT_F32)
+                y[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, voff + 4 * e, soff, 0));
+            else
+                y[e] = from_out16<OUT>(__builtin_amdgcn_raw_buffer_load_b16(rows, voff + 2 * e, soff, 0));
         }
-    }
+    return y;
 }
 template <int OUT>
-__device__ __forceinline__ void lora_store16(uint8_t *p, int64_t at, int n, bool vec, const float (&y)[16]) {
-    if constexpr (OUT == DT_F32) {
-        float *d = reinterpret_cast<float *>(p) + at;
-        if (vec && n == 16) {
+__device__ __forceinline__ void lora_store_some(__amdgpu_buffer_rsrc_t rows, uint32_t voff, uint32_t soff, int n,
+                                                const f32x4 &y) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                reinterpret_cast<f32x4 *>(d)[q] = f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e < n) d[e] = y[e];
+    for (int e = 0; e < 4; ++e)
+        if (e < n) {
+            if constexpr (OUT == DT_F32)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), rows, voff + 4 * e, soff, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16((unsigned short)to_out16<OUT>(y[e], false), rows, voff + 2 * e,
+                                                      soff, 0);
         }
-    } else {
-        uint16_t *d = reinterpret_cast<uint16_t *>(p) + at;
-        if (vec && n == 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = pack_out16<OUT>(y[2 * e], y[2 * e + 1]);
-            reinterpret_cast<u32x4 *>(d)[0] = u32x4{w[0], w[1], w[2], w[3]};
-            reinterpret_cast<u32x4 *>(d)[1] = u32x4{w[4], w[5], w[6], w[7]};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e < n) d[e] = (uint16_t)to_out16<OUT>(y[e], false);
-        }
-    }
 }
 
 // Few tokens: D of one token, 64 columns for a wave.  A column is a lane's dot product of
 // rank terms, in fp32 with h as it is: with a token an adapter, a column of the MFMA would
-// be all that it uses of one (64 tokens of 64 adapters, 4096 columns: 10.0 us so, and 5 us
+// be all that it uses of one (64 tokens of 64 adapters, 4096 columns: 10.0 us so, and 4.5
 // with a token for each wave).
 // Grid: x blocks of 256 columns, y tokens.
 template <int IT, int OUT, bool VEC>
@@ -530,45 +528,67 @@ __global__ void __launch_bounds__(1024) lora_one_kernel(LoraParams p) {
     else reinterpret_cast<uint16_t *>(p.D)[at] = (uint16_t)to_out16<OUT>(y, false);
 }
 
-// Many tokens: D of 64 tokens and an adapter at a time; a wave takes 64 columns.  Its four
-// row tiles interleave the columns by fours, so that a lane ends up with 16 consecutive
-// ones: row i of tile j is column 16 (i / 4) + 4 j + i % 4.
+// Tokens of a tile of the second product: with 64, the registers leave two waves a SIMD
+// instead of four (three past rank 32), whose loads, products and stores then follow one
+// another.  us, 64 and 32 tokens, N = 4096 in bf16: 512 tokens 9 and 6, 2048 of rank 32 11.6
+// and 10.2, 8192 of rank 16 37 and 33 (4.1 TB/s), 4096 of rank 64 28 and 28.
+constexpr int kLoraUpTokens = 32;
+
+// Many tokens: D of a tile and an adapter at a time; a wave takes 64 columns.  Its four
+// column tiles interleave the columns by ones, column i of tile j being 4 i + j, so that a
+// lane ends up with four consecutive columns of four tokens, and 16 lanes with 128 bytes (of
+// a 16-bit type) of a row.
 //
 // h goes into the MFMA as its 16-bit values, one MFMA after the other on the same part of
 // B.  B's 32 RS ranks stay in registers for the tile's tokens (larger ranks read B for
-// every 16 tokens).  C, which no id decides, is asked for first.
+// every 16 tokens).  C, which no id decides, is asked for first.  A row of the MFMA holds one
+// token: those of other groups are computed on what is there, and not kept.
+// What bounds it at rank 64 is B, read by rows of 16 bytes for each tile (half of the address
+// path's time, and as many bytes from L2 as C and D have).
 // Grid: x blocks of 256 columns (so that an XCD's L2 holds few blocks of B: 27.4 us, tiles
 // first 29.3), z tiles.
 template <int IT, int OUT, int RS, bool VEC>
-__global__ void __launch_bounds__(256, 2) lora_up_kernel(LoraParams p) {
-    constexpr int SUBS = 4, PARTS = kLoraParts<OUT>, CW = OUT == DT_F32 ? 4 : 2, OSZ = CW;
+__global__ void __launch_bounds__(256, OUT == DT_F32 ? 2 : RS == 2 ? 3 : 4) lora_up_kernel(LoraParams p) {
+    constexpr int SUBS = kLoraUpTokens / 16, PARTS = kLoraParts<OUT>, OSZ = OUT == DT_F32 ? 4 : 2;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * 256 + wave * 64;
     if (n0 >= p.N) return;
     const int t0 = blockIdx.z * 16 * SUBS, lg = lane >> 4;
     const int id = lora_id(p, t0, 16 * SUBS, lane);
-    const int64_t n = n0 + 16 * lg;  // this lane's 16 columns
-    const int left = (int)min(max(p.N - n, (int64_t)0), (int64_t)16);
-    const bool whole = p.vec_cd && left == 16;
-    const int chunks = p.ldh / 8;    // of 8 ranks
-    auto token = [&](int s) { return t0 + 16 * s + (lane & 15); };
-    u32x4 cv[SUBS][CW];
+    const int64_t n = n0 + 4 * (lane & 15);  // this lane's four columns
+    const int left = (int)min(max(p.N - n, (int64_t)0), (int64_t)4);
+    const bool whole = p.vec_cd && left == 4;
+    const int wide = (p.ldh + 31) / 32;      // of 32 ranks
+    // Offsets in the tile's rows of C and D: 31 lines of 2^24 fp32 and a row of 2^19 stay
+    // below 2^32.  (64-bit addresses for each of them take the registers of B.)
+    auto rows = [&](const uint8_t *base, int64_t ld) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base) + (int64_t)t0 * ld * OSZ, (short)0,
+                                                 -1, 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t c_rows = rows(p.C, p.ldc), d_rows = rows(p.D, p.ldd);
+    const uint32_t c_at = (4u * lg * (uint32_t)p.ldc + (uint32_t)n) * OSZ;
+    const uint32_t d_at = (4u * lg * (uint32_t)p.ldd + (uint32_t)n) * OSZ;
+    const int tokens = p.T - t0 - 4 * lg;    // from this lane's first on
+    const __amdgpu_buffer_rsrc_t downs = __builtin_amdgcn_make_buffer_rsrc(p.down + t0, (short)0, -1, 0x00020000);
+    LoraQuad<OUT> cv[SUBS][4];
 #pragma unroll
     for (int s = 0; s < SUBS; ++s)
-        if (p.C && whole && token(s) < p.T) {
-            const u32x4 *c = reinterpret_cast<const u32x4 *>(p.C + ((int64_t)token(s) * p.ldc + n) * OSZ);
 #pragma unroll
-            for (int q = 0; q < CW; ++q) cv[s][q] = c[q];
+        for (int e = 0; e < 4; ++e) {
+            if (p.C && whole && 16 * s + e < tokens) {
+                const uint32_t at = (16u * s + e) * (uint32_t)p.ldc * OSZ;
+                if constexpr (OUT == DT_F32) cv[s][e] = __builtin_amdgcn_raw_buffer_load_b128(c_rows, c_at, at, 0);
+                else cv[s][e] = __builtin_amdgcn_raw_buffer_load_b64(c_rows, c_at, at, 0);
+            }
         }
     lora_groups(id, 0, 1, !p.in_place, [&](const LoraGroup &g) {
         const int rank = g.adapter < 0 ? 0 : lora_rank(p, g.adapter);
         const float scale = rank > 0 && p.scales ? p.scales[g.adapter] : 1.0f;
         const uint8_t *b[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t col = n0 + 16 * ((lane & 15) >> 2) + 4 * j + (lane & 3);
-            b[j] = p.B + ((int64_t)max(g.adapter, 0) * p.N + (col < p.N ? col : p.N - 1)) * p.ldb * 2;
-        }
+        for (int j = 0; j < 4; ++j)
+            b[j] = p.B + ((int64_t)max(g.adapter, 0) * p.N + min(n + j, (int64_t)p.N - 1)) * p.ldb * 2;
+        const uint64_t mine = g.members >> (4 * lg);  // bit 16 s + e: this lane's token
         u32x4 bv[RS][4];
         auto load_b = [&](int r0) {
 #pragma unroll
@@ -580,7 +600,6 @@ __global__ void __launch_bounds__(256, 2) lora_up_kernel(LoraParams p) {
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
             if (!(g.members >> (16 * s) & 0xffff)) continue;
-            const bool in = g.members >> (16 * s + (lane & 15)) & 1;
             f32x4 acc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -588,43 +607,45 @@ __global__ void __launch_bounds__(256, 2) lora_up_kernel(LoraParams p) {
                 if (rank > 32 * RS) load_b(r0);
                 u32x4 hv[RS][PARTS];
 #pragma unroll
-                for (int q = 0; q < RS; ++q) {
-                    const int c = r0 / 8 + 4 * q + lg;
+                for (int q = 0; q < RS; ++q)
 #pragma unroll
                     for (int k = 0; k < PARTS; ++k) {
                         hv[q][k] = u32x4{0u, 0u, 0u, 0u};
-                        if (in && c < chunks)
-                            hv[q][k] = *reinterpret_cast<const u32x4 *>(
-                                p.parts + ((int64_t)k * p.T + token(s)) * p.ldh + 8 * c);
+                        if (r0 / 32 + q < wide)
+                            hv[q][k] = reinterpret_cast<const u32x4 *>(
+                                p.parts)[lora_part<PARTS>(p, t0 + 16 * s, k, r0 / 8 + 4 * q) + lane];
                     }
-                }
 #pragma unroll
                 for (int q = 0; q < RS; ++q)
 #pragma unroll
                     for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[j] = mfma16_1<IT>(bv[q][j], hv[q][k], acc[j]);
+                        for (int j = 0; j < 4; ++j) acc[j] = mfma16_1<IT>(hv[q][k], bv[q][j], acc[j]);
             }
-            if (!in || left == 0) continue;
-            const int64_t t = token(s);
-            const float down = IT == IT_F16 && rank > 0 ? p.down[t] : 1.0f;
-            float y[16];
-            if (!p.C) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-            } else if (whole) {
-                lora_values<OUT>(cv[s], y);
-            } else {
-                lora_load_some<OUT>(p.C, t * p.ldc + n, left, y);
-            }
-            if (rank > 0) {
+            for (int e = 0; e < 4; ++e) {
+                if (!(mine >> (16 * s + e) & 1) || left == 0) continue;
+                const uint32_t c_row = (16u * s + e) * (uint32_t)p.ldc * OSZ;
+                const uint32_t d_row = (16u * s + e) * (uint32_t)p.ldd * OSZ;
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (p.C) y = whole ? lora_values<OUT>(cv[s][e]) : lora_load_some<OUT>(c_rows, c_at, c_row, left);
+                if (rank > 0) {
+                    const float down =
+                        IT == IT_F16 ? __uint_as_float(buf_load4(downs, 16u * lg, (16u * s + e) * 4u)) : 1.0f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float v = acc[e / 4][e % 4];
-                    y[e] += scale * (IT == IT_F16 ? v * down : v);
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = acc[j][e];
+                        y[j] += scale * (IT == IT_F16 ? v * down : v);
+                    }
                 }
+                if (!whole)
+                    lora_store_some<OUT>(d_rows, d_at, d_row, left, y);
+                else if constexpr (OUT == DT_F32)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), d_rows, d_at, d_row, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b64(
+                        u32x2{pack_out16<OUT>(y[0], y[1]), pack_out16<OUT>(y[2], y[3])}, d_rows, d_at, d_row, 0);
             }
-            lora_store16<OUT>(p.D, t * p.ldd + n, left, p.vec_cd, y);
         }
     });
 }

@@ -73,7 +73,7 @@ hipError_t launch_lora(const LoraParams &p, int out_dtype, bool few, bool vec_xa
     if (e != hipSuccess) return e;
     if (!few) {
         int lanes = 1;  // threads of a token, 8 ranks each
-        while (8 * lanes < p.ldh) lanes *= 2;
+        while (lanes < (p.ldh + 31) / 32 * 4) lanes *= 2;
         void *with_lanes[] = {&arg, &lanes};
         const void *k = out_dtype == DT_F32 ? (const void *)lora_parts_kernel<IT, 3>
                                             : (const void *)lora_parts_kernel<IT, 2>;
@@ -82,7 +82,7 @@ hipError_t launch_lora(const LoraParams &p, int out_dtype, bool few, bool vec_xa
     }
     const void *k = vec_b ? lora_up_of<IT, true>(few, out_dtype, p.rank)
                           : lora_up_of<IT, false>(few, out_dtype, p.rank);
-    return hipLaunchKernel(k, few ? dim3(columns, (unsigned)p.T) : dim3(columns, 1, tiles64), dim3(256),
+    return hipLaunchKernel(k, few ? dim3(columns, (unsigned)p.T) : dim3(columns, 1, (unsigned)cdiv(p.T, kLoraUpTokens)), dim3(256),
                            args, 0, s);
 }
 

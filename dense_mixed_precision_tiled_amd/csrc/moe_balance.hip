@@ -12,8 +12,10 @@
 //
 // In the gradient f is the same for every token and stays in registers.
 //
-// The first kernel is bound by its vector instructions (the choice of eight experts takes
-// about 120 for a token's lanes), the gradient by memory.
+// The first kernel is bound by its vector instructions (about 230 for four tokens of 64
+// experts, top 8, most of them the choice), the gradient by memory.  65536 tokens of 64
+// experts, top 8: 12.0 us (1.4 TB/s), 4.5 for the sums over the workgroups, and 8.8 for a
+// gradient in bf16 (2.9 TB/s); 1024 tokens of 8 experts 4.8, 2.7 and 3.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -617,7 +617,8 @@ int gemm_validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const flo
  *                content, owned by the caller, written by the call.  A call must not overlap
  *                another one (or a graph's replay) that uses the same workspace, unless the
  *                caller orders them.
- * The call enqueues two kernels, three past 256 tokens, and allocates nothing, so it can be
+ * The call enqueues one kernel (few tokens, rank 32 at most), two, or past 256 tokens three,
+ * and allocates nothing, so it can be
  * captured into a HIP graph; which tokens use which adapter is found on the device, and a
  * replay follows the ids of its own time.  Tokens do not touch each other: what an adapter
  * holds (an Inf, a NaN) reaches its own tokens only.  The same call gives the same bits.
@@ -719,7 +720,8 @@ int gemm_validate_lora(int64_t T, const gemm_lora_t *lora, const void *X, int64_
  * Speed: 16-byte accesses where the operands' base pointers and lines are whole 16 bytes
  * (for wgrad G and Q, for the others X, G, D and Q); element by element otherwise.  With
  * them, bytes of the padding next to a row's last element are read (up to 15 past the
- * last row's), and never matter.
+ * last row's), and never matter.  wgrad reads S in aligned dwords: up to 3 bytes beside its
+ * rows, also before the first.
  *
  * Errors: GEMM_ERR_INVALID_DIM (a dimension negative or above 2^31-1), GEMM_ERR_INVALID_LD
  * (a line shorter than its row, or longer than 2^40 elements), GEMM_ERR_NULL_PTR,

@@ -323,3 +323,23 @@ def test_long_offsets():
                         w.ws.data_ptr(), w.size, stream()))
     w.dD.view.copy_(torch.as_strided(D, (T, N), (ld, 1)))
     w.check()
+
+
+@pytest.mark.parametrize("o", [F32, BF16])
+def test_long_offsets_of_prompts(o):
+    """The same past 256 tokens, at the longest lines: a tile's own rows reach 2 GiB."""
+    T, K, N, rank, adapters, ld = 300, 64, 72, 16, 10, 1 << 24
+    w = Lora(T, K, N, rank, adapters, BF16, o, ids="runs")
+
+    def spread(m):
+        buf = torch.empty((m.shape[0] - 1) * ld + m.shape[1], dtype=m.dtype, device="cuda")
+        torch.as_strided(buf, tuple(m.shape), (ld, 1)).copy_(m)
+        return buf
+
+    X, A, C = spread(w.X), spread(w.A), spread(w.C)
+    D = torch.empty_like(C)
+    lora = lg.GemmLora(K, N, adapters, rank, A.data_ptr(), ld, w.dB.ptr, w.dB.ld, 0, w.dscales.data_ptr())
+    ok(lg.gemm_lora_run(T, lora, X.data_ptr(), ld, w.dids.data_ptr(), C.data_ptr(), ld, D.data_ptr(), ld, BF16, o,
+                        w.ws.data_ptr(), w.size, stream()))
+    w.dD.view.copy_(torch.as_strided(D, (T, N), (ld, 1)))
+    w.check()
