@@ -297,10 +297,10 @@ inline int validate_lora_dims(int64_t T, const gemm_lora_t *l) {
 }
 
 // Up to this many tokens they are taken one by one and 16 at a time, else 64 (lora.hpp).
-// us on 4096 x 4096 in bf16, first against second way: packed prompts of 4 adapters, 128
-// tokens, rank 16 11.7 and 20.1, rank 64 25 and 24; 256 tokens 18.4 and 16.4, 41 and 19; 512
-// tokens 24 and 17, 59 and 19.  Tokens of 32 adapters in any order, as a decoding batch has
-// them: 256 tokens 21 and 167, 53 and 217; 512 tokens 33 and 170, 90 and 234.
+// us on 4096 x 4096 in bf16, first against second way: packed prompts of 4 adapters, 256
+// tokens, rank 16 17.4 and 19.5 (257), rank 64 40 and 23; 512 tokens 24 and 14.4, 59 and 17.3.
+// Tokens of 32 adapters in any order, as a decoding batch has them: 256 tokens 20 and 156, 53
+// and 191; 512 tokens 33 and 158, 90 and 199.
 constexpr int64_t kLoraFew = 256;
 // Parts of K that different workgroups take: with few tiles of tokens there are CUs to
 // spare, and an adapter's rows of A are long.
