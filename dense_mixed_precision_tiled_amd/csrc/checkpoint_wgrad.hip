@@ -213,7 +213,7 @@ int gemm_checkpoint_wgrad(int64_t M, int64_t N, int64_t K, const void *G, int64_
     g.K = (int)M;
     g.out_dtype = out_dtype;
     g.splits = (int)plan.splits;
-    g.k_per_split = (int)plan.per;
+    g.k_per_split = (int)(plan.per < M ? plan.per : M);  // (per may be 2^31)
     // groups of four elements in C and D's rows
     g.cd_vec = (uintptr_t)D % (4 * osz) == 0 && ldd % 4 == 0 &&
                (!C || ((uintptr_t)C % (4 * osz) == 0 && ldc % 4 == 0));
