@@ -12,6 +12,13 @@
 // depends on m moves whole 64-byte groups, so that half a wave's transposing reads, four
 // rows at 64 bytes, touch distinct banks; bit 0 keeps the widened values' writes apart,
 // whose lanes write every second chunk.
+//
+// What bounds it: the matrix units are busy 45% of the time at 4096^3.  In 64 tokens a wave
+// of the 256 x 256 tile issues 32 MFMAs and some 130 vector instructions, most of them
+// widening Q (sixteen times over, once for each tile row that reads it); the stages' barrier
+// leaves nothing else on the CU.  us, bf16 into fp32: 4096^3 135 without C (1.02 PFLOP/s; 131
+// for a product of bf16 operands of these layouts) and 151 with it; 128 x 128 tiles 184 there,
+// but 37 against 59 for 1024 x 4096 of 2048 tokens, where they fill the CUs.
 #pragma once
 
 #include "checkpoint.hpp"
