@@ -5,7 +5,7 @@
 // of a 16-bit type, 8 of Q), four lanes a block of 32.  The row of an item is found
 // with one multiplication, so that short and odd rows fill the waves too.  4096 x 16384
 // values of bf16 are packed in 41 us (5.0 TB/s, a copy's rate); D = G * gelu'(X^) of as many
-// takes 74 (4.6 TB/s; about 28 vector instructions for each value beside them).
+// takes 77 (4.4 TB/s; about 30 vector instructions for each value beside them).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -134,18 +134,20 @@ __global__ void __launch_bounds__(256) checkpoint_pack_kernel(CkParams p) {
     }
 }
 
-// exp(a^2 / 2) erfc(a / sqrt 2) / 2 for a >= 0 as a polynomial in t = 1 / (1 + 0.3 a),
-// fitted to the least largest error of its product with exp(-a^2 / 2) over a in [0, 18]
-// (Lawson's iteration on 4000 Chebyshev points): off by at most 5e-8 there, 2e-7 as
-// evaluated.  Past that the product is 0 in fp32.
+// exp(a^2 / 2) erfc(a / sqrt 2) / 2 for a >= 0 as a polynomial in t = 1 / (1 + 0.35 a),
+// fitted over a in [0, 14] to the least largest error relative to itself + a / sqrt(2 pi)
+// (Lawson's iteration on 4000 Chebyshev points): off by at most 9e-8 of that, 3.2e-7 as
+// evaluated.  Past that the exponential it is multiplied with is 0 in fp32.
 __device__ __forceinline__ float ck_tail(float a) {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.3f, 1.0f));
-    float r = -0.147075355052948f;
-    r = __builtin_fmaf(r, t, 0.6868159174919128f);
-    r = __builtin_fmaf(r, t, -0.5748485922813416f);
-    r = __builtin_fmaf(r, t, 0.5226098299026489f);
-    r = __builtin_fmaf(r, t, -0.0027446860913187265f);
-    r = __builtin_fmaf(r, t, 0.015242913737893105f);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.35f, 1.0f));
+    float r = 0.044291477650403976f;
+    r = __builtin_fmaf(r, t, -0.18242865800857544f);
+    r = __builtin_fmaf(r, t, 0.2062307447195053f);
+    r = __builtin_fmaf(r, t, 0.014985134825110435f);
+    r = __builtin_fmaf(r, t, 0.13894817233085632f);
+    r = __builtin_fmaf(r, t, 0.1384863704442978f);
+    r = __builtin_fmaf(r, t, 0.13946348428726196f);
+    r = __builtin_fmaf(r, t, 2.3313299607252702e-05f);
     return r;
 }
 
@@ -155,11 +157,13 @@ __device__ __forceinline__ float ck_slope(float x) {
     if constexpr (ACT == ACT_RELU) {
         return x != x ? x : (x > 0.0f ? 1.0f : 0.0f);
     } else if constexpr (ACT == ACT_GELU) {
-        // Phi(x) + x phi(x) = 1/2 +- (1/2 - exp(-a^2 / 2) (tail(a) - a / sqrt(2 pi))), a = |x|
-        // (x is finite, or NaN)
+        // Phi(x) + x phi(x), from y = Phi(-a) - a phi(a) = exp(-a^2 / 2) (tail(a) - a / sqrt(2 pi)),
+        // a = |x|: y itself for x < 0, so that it keeps its relative precision as it goes to 0,
+        // and 1 - y for the others.  (x is finite, or NaN; x^2 is exact, x having seven bits, and
+        // its product with the constant is rounded: x^2 2^-24 relatively)
         const float a = __builtin_fabsf(x), e = __builtin_amdgcn_exp2f(x * x * -0.72134752f);
         const float r = __builtin_fmaf(a, -0.39894228f, ck_tail(a));
-        return 0.5f + __builtin_copysignf(__builtin_fmaf(-e, r, 0.5f), x);
+        return x < 0.0f ? e * r : __builtin_fmaf(-e, r, 1.0f);
     } else {
         // from exp(-|x|), so that neither s nor 1 - s cancels
         const float e = __expf(-__builtin_fabsf(x));

@@ -700,7 +700,9 @@ int gemm_validate_lora(int64_t T, const gemm_lora_t *lora, const void *X, int64_
  *   activation   GEMM_ACT_RELU (act' = 1 for X^ > 0, else 0; G * NaN where X^ is NaN),
  *                GEMM_ACT_GELU (Phi(x) + x phi(x)) or GEMM_ACT_SILU (s + x s (1 - s),
  *                s = 1 / (1 + exp(-x)))
- * Between X^ and the rounding everything is fp32: act' is within 1e-6 absolutely.
+ * Between X^ and the rounding everything is fp32: act' is within 1e-6 absolutely, and for
+ * X^ < 0, where it goes to 0, within 2^-20 + x^2 2^-24 (SiLU: 2^-20 + |x| 2^-23) of the sum of its
+ * two terms' magnitudes (what is below 2^-126 of an exponential may be 0).
  *
  * gemm_checkpoint_wgrad: a linear layer's weight gradient, D = G^T X^ + C:
  *   D(n,k) = sum_m G(m,n) X^(m,k) + C(n,k)

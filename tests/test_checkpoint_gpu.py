@@ -465,3 +465,44 @@ def test_wgrad_tiles_captured():
         graph.replay()
         assert torch.equal(w.dD.get(), eager)
         w.call()
+
+
+@pytest.mark.parametrize("a", [lg.GEMM_ACT_GELU, lg.GEMM_ACT_SILU])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_act_grad_tails(dtype, a):
+    """The slope keeps its relative precision where it goes to 0, at every value of the
+    format from -2^8 to 2^8, on G = 1 (fp16: 1024, whose subnormal values are rounded to 2^-25).
+
+    With p = Phi(x), f = |x| phi(x) (SiLU: s, |x| s (1 - s)), for x < 0: (2^-20 + x^2 2^-24) (p + f)
+    (SiLU: 2^-20 + |x| 2^-23).  An exponential's argument h is rounded, and its constant, to
+    1.5 2^-24 h; the exponential and the reciprocal add 2^-23 each, the polynomial 4e-7, five
+    more operations 2^-24 each.  What is below 2^-126 of an exponential may be 0: 2^-122 of GELU
+    (|x| < 14 there), 2^-118 of SiLU (|x| < 88).  For x >= 0 1e-6, absolutely."""
+    k = np.arange(-20, 9)  # S - 127
+    Q = np.tile(np.arange(-127, 129).clip(max=127).astype(np.int8), (len(k), 1))
+    S = np.tile((k + 127).astype(np.uint8)[:, None], (1, 8))
+    V = ck.values(Q, S)
+    g = 1024.0 if dtype == F16 else 1.0
+    M, K = Q.shape
+    dQ, dS = Lines(M, K, torch.int8, fill=torch.from_numpy(Q)), Lines(M, 8, torch.uint8, fill=torch.from_numpy(S))
+    dG, dD = Lines(M, K, TORCH[dtype], fill=torch.full((M, K), g)), Lines(M, K, TORCH[dtype])
+    ok(lg.gemm_checkpoint_act_grad(M, K, dQ.ptr, K, dS.ptr, 8, dG.ptr, K, a, dD.ptr, K, dtype, stream()))
+    got = dD.get().double().numpy()
+    n = np.abs(V)
+    if a == lg.GEMM_ACT_GELU:
+        p = 0.5 * np.vectorize(math.erfc)(n / math.sqrt(2.0))
+        f = n * np.exp(-n * n / 2) / math.sqrt(2 * math.pi)
+        rel, low = 2.0 ** -20 + V * V * 2.0 ** -24, 2.0 ** -122
+    else:
+        p = np.exp(-n) / (1 + np.exp(-n))
+        f = n * p * (1 - p)
+        rel, low = 2.0 ** -20 + n * 2.0 ** -23, 2.0 ** -118
+    want = g * np.where(V < 0, p - f, 1 - p + f)  # both forms of the slope, without cancellation
+    r = HALF_STEP[dtype]
+    slope = g * (np.where(V < 0, rel * (p + f), 1e-6) + low)
+    tol = r * np.abs(want) + (1 + r) * slope + TINY[dtype]
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+    if dtype != F16:  # down to x = -12 the negative side is nothing but this slope
+        far = (V <= -6) & (V >= -12)
+        assert far.sum() > 100
+        assert (np.abs(got - want)[far] <= (r + 1.1e-5) * np.abs(want[far])).all()
