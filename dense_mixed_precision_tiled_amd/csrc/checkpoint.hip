@@ -151,11 +151,12 @@ __device__ __forceinline__ float ck_tail(float a) {
     return r;
 }
 
-// The slope of an activation function.
+// g times the slope of an activation function at x.
 template <int ACT>
-__device__ __forceinline__ float ck_slope(float x) {
+__device__ __forceinline__ float ck_grad(float g, float x) {
     if constexpr (ACT == ACT_RELU) {
-        return x != x ? x : (x > 0.0f ? 1.0f : 0.0f);
+        // selected: an Inf or a NaN of g where the slope is 0 has no part in it
+        return x > 0.0f ? g : (x != x ? x : 0.0f);
     } else if constexpr (ACT == ACT_GELU) {
         // Phi(x) + x phi(x), from y = Phi(-a) - a phi(a) = exp(-a^2 / 2) (tail(a) - a / sqrt(2 pi)),
         // a = |x|: y itself for x < 0, so that it keeps its relative precision as it goes to 0,
@@ -163,12 +164,12 @@ __device__ __forceinline__ float ck_slope(float x) {
         // its product with the constant is rounded: x^2 2^-24 relatively)
         const float a = __builtin_fabsf(x), e = __builtin_amdgcn_exp2f(x * x * -0.72134752f);
         const float r = __builtin_fmaf(a, -0.39894228f, ck_tail(a));
-        return x < 0.0f ? e * r : __builtin_fmaf(-e, r, 1.0f);
+        return g * (x < 0.0f ? e * r : __builtin_fmaf(-e, r, 1.0f));
     } else {
         // from exp(-|x|), so that neither s nor 1 - s cancels
         const float e = __expf(-__builtin_fabsf(x));
         const float high = __builtin_amdgcn_rcpf(1.0f + e), low = e * high;
-        return __builtin_fmaf(x * high, low, x < 0.0f ? low : high);
+        return g * __builtin_fmaf(x * high, low, x < 0.0f ? low : high);
     }
 }
 
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(256) checkpoint_use_kernel(CkParams p) {
         for (int e = 0; e < 8; ++e) {
             const float x = ck_int(q[u][e / 4], e % 4) * unit;
             if constexpr (ACT == ACT_NONE) y[e] = x;
-            else y[e] = ck_value<DT>(g[u], e) * ck_slope<ACT>(x);
+            else y[e] = ck_grad<ACT>(ck_value<DT>(g[u], e), x);
         }
         if (base + u * 256u >= p.items) continue;
         const int64_t k = (int64_t)lane[u] * 8;

@@ -697,7 +697,7 @@ int gemm_validate_lora(int64_t T, const gemm_lora_t *lora, const void *X, int64_
  *
  * gemm_checkpoint_act_grad: D = G * act'(X^), rounded once; G and D of `dtype`, M x K,
  * row-major.  D == G with ldd == ldg is the in-place update.
- *   activation   GEMM_ACT_RELU (act' = 1 for X^ > 0, else 0; G * NaN where X^ is NaN),
+ *   activation   GEMM_ACT_RELU (D = G for X^ > 0, else 0, whatever G holds; NaN where X^ is),
  *                GEMM_ACT_GELU (Phi(x) + x phi(x)) or GEMM_ACT_SILU (s + x s (1 - s),
  *                s = 1 / (1 + exp(-x)))
  * Between X^ and the rounding everything is fp32: act' is within 1e-6 absolutely, and for

@@ -506,3 +506,22 @@ def test_act_grad_tails(dtype, a):
         far = (V <= -6) & (V >= -12)
         assert far.sum() > 100
         assert (np.abs(got - want)[far] <= (r + 1.1e-5) * np.abs(want[far])).all()
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_relu_grad_selects(dtype, how):
+    """ReLU's gradient takes G or 0: an Inf or a NaN of G where X^ <= 0 is left out."""
+    inf, nan = float("inf"), float("nan")
+    Q = np.tile(np.array([1, -1, 0, 64, -64, 127, -127, 5], np.int8), (4, 5))
+    S = np.full((4, 2), 127, np.uint8)
+    S[2, 0], S[3] = 255, 0
+    V = ck.values(Q, S)
+    G = torch.tensor([inf, -inf, nan, 2.0, inf, nan, nan, -inf, 0.0, -3.0]).repeat(4, 4).to(TORCH[dtype])
+    ldx, ldq, lds, sx, sq = layout(40, dtype, how)
+    dQ, dS = Lines(4, 40, torch.int8, ldq, sq, torch.from_numpy(Q)), Lines(4, 2, torch.uint8, lds, sq, torch.from_numpy(S))
+    dG, dD = Lines(4, 40, TORCH[dtype], ldx, sx, G), Lines(4, 40, TORCH[dtype], ldx, sx)
+    ok(lg.gemm_checkpoint_act_grad(4, 40, dQ.ptr, ldq, dS.ptr, lds, dG.ptr, ldx, lg.GEMM_ACT_RELU, dD.ptr, ldx,
+                                   dtype, stream()))
+    want = np.where(np.isnan(V), np.nan, np.where(V > 0, G.double().numpy(), 0.0))
+    assert np.array_equal(dD.get().double().numpy(), want, equal_nan=True)
