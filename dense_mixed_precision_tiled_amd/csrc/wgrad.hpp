@@ -104,8 +104,8 @@ struct WgradLoop {
 
     // First token of tile t.  A ragged last tile starts where it ends with the part's last
     // token (M is at least 64), so that no lane's offset depends on the tile: its first
-    // rows, `again` of them, were in the tile before, and become 0 in G's stage.  They meet
-    // finite values of Q, or a NaN that made its columns NaN before.
+    // rows, `again` of them, were in the tile before, and become 0 in both stages (in G's alone,
+    // an X^ that is Inf, as fp16 has it past 65504, would make 0 * Inf = NaN of them).
     __device__ __forceinline__ int64_t first(int t) const {
         return min(m_beg + (int64_t)t * BK, m_end - BK);
     }
@@ -170,10 +170,12 @@ struct WgradLoop {
         const int m = q_row(i), c = 2 * (tid % QC) + h;
         reinterpret_cast<u32x4 *>(lds)[2 * SA + stage * SB + m * CB + (c ^ wgrad_slot<CB>(m, c))] = w;
     }
-    // the first rows of G's stage become 0
-    __device__ __forceinline__ void zero_a(int stage, int rows) const {
-        for (int i = tid; i < rows * CA; i += THREADS)
-            reinterpret_cast<u32x4 *>(lds)[stage * SA + i] = u32x4{0u, 0u, 0u, 0u};
+    // the first rows of a stage become 0
+    __device__ __forceinline__ void zero(int stage, int rows) const {
+        u32x4 *const a = reinterpret_cast<u32x4 *>(lds) + stage * SA;
+        u32x4 *const b = reinterpret_cast<u32x4 *>(lds) + 2 * SA + stage * SB;
+        for (int i = tid; i < rows * CA; i += THREADS) a[i] = u32x4{0u, 0u, 0u, 0u};
+        for (int i = tid; i < rows * CB; i += THREADS) b[i] = u32x4{0u, 0u, 0u, 0u};
     }
 
     __device__ __forceinline__ void run(f32x16 (&acc)[TM][TN]) {
@@ -221,7 +223,7 @@ struct WgradLoop {
         });
         __syncthreads();
         if (again(0) > 0) {
-            zero_a(0, again(0));
+            zero(0, again(0));
             __syncthreads();
         }
         Unroll<0, TM + TN>::run([&](auto f) { read(Zero{}, Zero{}, Zero{}, f); });
@@ -256,7 +258,7 @@ struct WgradLoop {
                     __builtin_amdgcn_sched_barrier(0);
                     load_b(min(t + 3, last));
                     if (t + 1 == last && again(last) > 0) {
-                        zero_a(CUR ^ 1, again(last));
+                        zero(CUR ^ 1, again(last));
                         __syncthreads();
                     }
                     __builtin_amdgcn_sched_barrier(0);

@@ -525,3 +525,39 @@ def test_relu_grad_selects(dtype, how):
                                    dtype, stream()))
     want = np.where(np.isnan(V), np.nan, np.where(V > 0, G.double().numpy(), 0.0))
     assert np.array_equal(dD.get().double().numpy(), want, equal_nan=True)
+
+
+def overflowing(M, N, K, tokens, how):
+    """fp16 call of integers in which the first block of each of `tokens` lies past 65504, in
+    values of both signs; (call, D by the definition)."""
+    w = Wgrad(M, N, K, F16, F32, how=how, ints=True)
+    for i, m in enumerate(tokens):
+        w.S[m, 0] = 127 + 17
+        w.Q[m, :32] = np.tile([64, -64, 100, -127], 8)[:min(K, 32)]
+        w.G[m] = torch.tensor([3.0, -2.0, 0.0, 1.0]).repeat(N // 4 + 1)[i:i + N].half()
+    w.dS.view.copy_(torch.from_numpy(w.S))
+    w.dQ.view.copy_(torch.from_numpy(w.Q))
+    w.dG.view.copy_(w.G)
+    V = ck.values(w.Q, w.S)
+    V = np.where(np.abs(V) > 65519, np.copysign(np.inf, V), V)
+    G = w.G.double().numpy()
+    hit = list(tokens)
+    rest = np.setdiff1d(np.arange(M), hit)
+    want = G[rest].T @ V[rest]
+    with np.errstate(invalid="ignore"):
+        for m in hit:
+            want = want + G[m][:, None] * V[m][None, :]
+    return w, want
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("M,N,K,back", [
+    (200, 100, 192, [20]), (200, 200, 192, [1]), (200, 200, 192, [64, 190]), (1351, 200, 200, [50]),
+    (8200, 1530, 1540, [20]),  # parts of 256 x 256
+    (200, 100, 192, [20, 30])])
+def test_wgrad_overflowing_values_in_tiles(M, N, K, back, how):
+    """Values past fp16's range are Inf, with their sign, wherever their token lies: also in the
+    rows that the last step of a tile takes once more (the last 64 of a ragged M)."""
+    w, want = overflowing(M, N, K, [M - b for b in back], how)
+    assert np.isinf(want[:, :32]).any() and np.isfinite(want[:, 32:]).all()
+    assert np.array_equal(w.call().dD.get().double().numpy(), want, equal_nan=True)
