@@ -122,14 +122,16 @@ __global__ void __launch_bounds__(64 * kThinWaves, 2) wgrad_thin_kernel(WgradPar
         if (m0 > m_beg) __syncthreads();  // the last stretch's reads are done
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            // rows past the last: 0, which Q's repeated rows meet
+            // rows past the last: 0
             const int at = i * THREADS + tid, m = at / CA, c = at % CA;
             smem[m * CA + (c ^ wgrad_slot<CA>(m, c))] = m <= last ? g[i] : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int at = i * THREADS + tid, m = at / 4, b = at % 4;
-            units[b * P + (m ^ (8 * b))] = ck_unit(u[i]);
+            // (tokens past the last, for which the last one's Q is read, are 0 on this side too: an
+            // X^ that is Inf, as fp16 has it past 65504, would make 0 * Inf = NaN of them)
+            units[b * P + (m ^ (8 * b))] = m <= last ? ck_unit(u[i]) : 0.0f;
         }
         __syncthreads();
         for (int s0 = 0; s0 < steps; s0 += 4) {

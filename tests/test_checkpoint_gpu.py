@@ -561,3 +561,14 @@ def test_wgrad_overflowing_values_in_tiles(M, N, K, back, how):
     w, want = overflowing(M, N, K, [M - b for b in back], how)
     assert np.isinf(want[:, :32]).any() and np.isfinite(want[:, 32:]).all()
     assert np.array_equal(w.call().dD.get().double().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("M,N,K,back", [
+    (201, 16, 192, [1]), (201, 60, 192, [1]), (1037, 20, 300, [1]), (1037, 60, 300, [1, 13]), (201, 32, 192, [9, 40]),
+    (9000, 33, 130, [1])])
+def test_wgrad_overflowing_values_of_few_outputs(M, N, K, back, how):
+    """The same for few outputs, whose last step of 16 tokens repeats the last one."""
+    w, want = overflowing(M, N, K, [M - b for b in back], how)
+    assert np.isinf(want[:, :32]).any() and np.isfinite(want[:, 32:]).all()
+    assert np.array_equal(w.call().dD.get().double().numpy(), want, equal_nan=True)
