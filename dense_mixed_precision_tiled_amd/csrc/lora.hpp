@@ -279,7 +279,8 @@ __device__ __forceinline__ int lora_exponent(float m) {
 }
 
 // Eight values (times a power of two) as PARTS 16-bit values each whose sum they are.  A
-// value that is not finite has no rest.
+// value that is not finite has no rest.  A finite one past bf16's largest keeps that as its
+// first part (rounded, it would be Inf, and its rest -Inf).
 template <int IT, int PARTS>
 __device__ __forceinline__ void lora_split(const float (&v)[8], float up, u32x4 (&w)[PARTS]) {
     constexpr int DT = IT == IT_F16 ? DT_F16 : DT_BF16;
@@ -288,7 +289,9 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], float up, u32x4 
         float a = IT == IT_F16 ? v[e] * up : v[e], b = IT == IT_F16 ? v[e + 1] * up : v[e + 1];
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
-            uint32_t x = to_out16<DT>(a, false), y = to_out16<DT>(b, false);
+            const bool bf = IT == IT_BF16 && q == 0;
+            uint32_t x = to_out16<DT>(a, bf && __builtin_isfinite(a));
+            uint32_t y = to_out16<DT>(b, bf && __builtin_isfinite(b));
             if (q > 0) {
                 x = a != a ? 0u : x;
                 y = b != b ? 0u : y;

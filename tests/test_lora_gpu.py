@@ -343,3 +343,22 @@ def test_long_offsets_of_prompts(o):
                         w.ws.data_ptr(), w.size, stream()))
     w.dD.view.copy_(torch.as_strided(D, (T, N), (ld, 1)))
     w.check()
+
+
+@pytest.mark.parametrize("o", [F32, BF16])
+@pytest.mark.parametrize("T", [20, 300])
+def test_bf16_inner_values_next_to_the_largest(T, o):
+    """h between bf16's largest finite value and fp32's; the scale brings the result back."""
+    w = Lora(T, 64, 40, 16, 3, BF16, o, c=False)
+    w.X[:, :], w.A[:, :] = 0.0, 0.0
+    w.X[:, :2] = 2.0 ** 64
+    w.A[::2, 0], w.A[::2, 1] = 2.0 ** 63 * (2 - 2.0 ** -7), 2.0 ** 55 * 1.5  # 2^127 (2 - 2^-7 + 1.5 2^-8)
+    w.A[1::4] = -w.A[::4]
+    w.B = (w.B.float() * 2.0 ** -5).bfloat16()
+    w.scales = w.scales * 2.0 ** -100
+    for d, v in ((w.dX, w.X), (w.dA, w.A), (w.dB, w.B)):
+        d.view.copy_(v)
+    w.dscales.copy_(w.scales)
+    h = float(w.A[0].double() @ w.X[0].double())
+    assert torch.tensor(h).isfinite() and torch.tensor(h).bfloat16().isinf()
+    w.call().check()
