@@ -271,11 +271,13 @@ __global__ void __launch_bounds__(256) lora_down_tile_kernel(LoraParams p) {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float lora_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// fp16: the exponent that brings a token's largest |h| to [2^8, 2^9).  (A largest value
-// below 2^-118 is taken as that; Inf and NaN stay so.)
+// fp16: the exponent that brings a token's largest |h| to [2^13, 2^14).  fp16's least step,
+// 2^-24, is then 2^-37 of it at most, half of which is lost, and the second product's sums (rank
+// 256, B below 2^16) stay below 2^38.  (A largest value below 2^-113 is taken as that; Inf and NaN
+// stay so.)
 __device__ __forceinline__ int lora_exponent(float m) {
     const int e = (int)(__float_as_uint(m) >> 23) - 127;
-    return min(max(8 - e, -119), 126);
+    return min(13 - e, 126);
 }
 
 // Eight values (times a power of two) as PARTS 16-bit values each whose sum they are.  A

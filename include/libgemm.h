@@ -626,7 +626,7 @@ int gemm_validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const flo
  * product takes h = x A^T as a sum of values of in_dtype: two of them for a 16-bit D (16
  * significant bits for bf16, 22 for fp16), three for an fp32 D (24 and 33).  fp16 values are
  * those of h times a power of two that follows the token's largest |h|, so h may lie anywhere
- * in fp32's range, and what is below 2^-34 (fp32 D: 2^-38) of that largest value is lost.
+ * in fp32's range, and what is below 2^-38 of that largest value is lost.
  *
  * Speed: 16-byte loads of X and A where both are 16-byte aligned with lines of whole 16
  * bytes, of B alike, and (past 256 tokens) of C and D; element by element otherwise.  Up to

@@ -362,3 +362,35 @@ def test_bf16_inner_values_next_to_the_largest(T, o):
     h = float(w.A[0].double() @ w.X[0].double())
     assert torch.tensor(h).isfinite() and torch.tensor(h).bfloat16().isinf()
     w.call().check()
+
+
+@pytest.mark.parametrize("o", [F32, F16, BF16])
+@pytest.mark.parametrize("T", [20, 300])
+def test_fp16_inner_values_beside_a_much_larger_one(T, o):
+    """A rank whose h is far below the token's largest keeps its documented share: columns of D
+    that use it alone are right but for 2^-38 of that largest value."""
+    w = Lora(T, 64, 40, 16, 3, F16, o, c=False, ids=[t % 3 for t in range(T)])
+    if o == F16:
+        w.scales = w.scales * 2.0 ** -8  # D of the largest within its range
+        w.dscales.copy_(w.scales)
+    w.X[:, :], w.A[:, :], w.B[:, :] = 0.0, 0.0, 0.0
+    w.X[:, 0], w.X[:, 1] = 2.0 ** 10, (1 + torch.arange(T) / 512).half()
+    w.A.view(3, 16, 64)[:, 0, 0] = 2.0 ** 10                # h0 = 2^20
+    for r in range(1, 16):                                  # h_r from 2^4 down to 2^-10
+        w.A.view(3, 16, 64)[:, r, 1] = 2.0 ** (5 - r) * (1 + r / 16)
+    for n in range(40):                                     # column n uses one rank
+        w.B.view(3, 40, 16)[:, n, n % 16] = 1.0 + n / 64
+    for d, v in ((w.dX, w.X), (w.dA, w.A), (w.dB, w.B)):
+        d.view.copy_(v)
+    got = w.call().dD.get().double().numpy()
+    h = w.A.double().view(3, 16, 64)[0].numpy() @ w.X.double().numpy().T       # the three adapters are alike
+    b = w.B.double().view(3, 40, 16)[0].numpy()
+    for t in range(T):
+        s = float(w.scales[t % 3])
+        want = s * (b @ h[:, t])
+        # h's parts, a rounding of h and of the two products, and the output's
+        parts = (3 if o == F32 else 2) * 11
+        tol = np.abs(b) @ np.abs(h[:, t]) * s * (2.0 ** -parts + 4 * 2.0 ** -24) + \
+            s * np.abs(b).sum(1) * 2.0 ** -38 * np.abs(h[:, t]).max()
+        tol = 1.01 * tol + HALF_STEP[o] * np.abs(want) + TINY[o]
+        assert (np.abs(got[t] - want) <= tol).all(), np.max(np.abs(got[t] - want) / tol)
