@@ -394,3 +394,38 @@ def test_fp16_inner_values_beside_a_much_larger_one(T, o):
             s * np.abs(b).sum(1) * 2.0 ** -38 * np.abs(h[:, t]).max()
         tol = 1.01 * tol + HALF_STEP[o] * np.abs(want) + TINY[o]
         assert (np.abs(got[t] - want) <= tol).all(), np.max(np.abs(got[t] - want) / tol)
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("i,o", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("T", [16, 80, 300])
+def test_infinite_weights_give_infinities(T, i, o, how):
+    """An Inf in B meets h as one number: D is Inf with the sign of h B, NaN only where h is 0 or
+    two of them cancel.  (For 300 tokens h comes in parts, some of which are 0.)"""
+    N = 1100
+    w = Lora(T, 64, N, 40 if T == 300 else 16, 4, i, o, how, ids=[t % 5 - 1 for t in range(T)], ints=True)
+    clean = w.call().dD.get()
+    r = w.rank
+    w.B[1 * N + 11, 4] = float("inf")
+    w.B[1 * N + 1099, r - 1] = float("-inf")
+    w.B[2 * N + 7, 0], w.B[2 * N + 7, 1] = float("inf"), float("inf")
+    w.X[3] = 0.0  # a token of adapter 2 with h = 0
+    w.dB.view.copy_(w.B)
+    w.dX.view.copy_(w.X)
+    got = w.call().dD.get()
+    X, A, B = w.X.double(), w.A.double().view(4, r, 64), w.B.double().view(4, N, r)
+    for t in range(T):
+        a = t % 5 - 1
+        if a not in (1, 2):
+            assert torch.equal(got[t], clean[t])
+            continue
+        bad = [11, 1099] if a == 1 else [7]
+        keep = [n for n in range(N) if n not in bad]
+        if t != 3:
+            assert torch.equal(got[t, keep], clean[t, keep])
+        h = A[a] @ X[t]
+        want = (B[a][bad] * h).sum(1)  # Inf, -Inf or NaN
+        assert not want.isfinite().any()
+        assert np.array_equal(got[t, bad].double().numpy(), want.numpy(), equal_nan=True)
+    w.call(w.dC)  # and in place
+    assert np.array_equal(w.dC.get().double().numpy(), got.double().numpy(), equal_nan=True)
