@@ -10,7 +10,8 @@
 // registers over a thread's tokens; then the groups of a wave, the waves of a workgroup
 // and, in the second kernel, the workgroups are added up in a fixed order.
 //
-// In the gradient f is the same for every token and stays in registers.
+// In the gradient f is the same for every token and stays in registers; p is made from lse and
+// brought to the sum 1.
 //
 // The first kernel is bound by its vector instructions (about 230 for four tokens of 64
 // experts, top 8, most of them the choice), the gradient by memory.  65536 tokens of 64
@@ -350,15 +351,23 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(BalanceParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) y[i] = 0.0f;
         } else {
-            float l[V], dot = 0.0f;
+            // p = exp(l - lse) over its sum: lse is rounded, and where it is large beside log E its
+            // rounding is a factor that all of a row's p share (E, for logits alike past 2^27 or so)
+            float l[V], dot = 0.0f, sum = 0.0f;
             balance_load<V, VEC>(p.logits + t * p.ldl, e0, p.E, l);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 // (an expert at -Inf, and those past E, have none; NaN - lse is NaN)
                 l[i] = balance_exp(l[i] - lse);
+                sum += l[i];
                 dot = __builtin_fmaf(f[i], l[i], dot);
             }
+            sum = group_sum<G>(sum);
             dot = group_sum<G>(dot);
+            const float inv = __builtin_amdgcn_rcpf(sum);
+            dot *= inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[i] *= inv;
 #pragma unroll
             for (int i = 0; i < V; ++i) y[i] = g * l[i] * __builtin_fmaf(a, f[i] - dot, b * lse);
         }

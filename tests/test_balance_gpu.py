@@ -260,3 +260,41 @@ def test_captured_follows_the_logits():
         replayed = b.check().get()
         b.call()
         assert all(torch.equal(x, y) for x, y in zip(b.get(), replayed))
+
+
+def gradient(l, topk, balance, z, g):
+    """The gradient by the definition in 64 bits, and |terms| of its bracket."""
+    T, E = l.shape
+    x = np.exp(l - l.max(1, keepdims=True))
+    p = x / x.sum(1, keepdims=True)
+    lse = np.log(x.sum(1)) + l.max(1)
+    counts = np.zeros(E)
+    for t in range(T):
+        for j in sorted(range(E), key=lambda j: (-l[t, j], j))[:topk]:
+            counts[j] += 1
+    f = counts / (T * topk)
+    fp = (p @ f)[:, None]
+    pull = abs(balance) * E * (f + fp) + 2 * abs(z) * np.abs(lse)[:, None]
+    return g / T * p * (balance * E * (f - fp) + 2 * z * lse[:, None]), abs(g) / T * p * pull
+
+
+@pytest.mark.parametrize("far", [0.0, -1e4, 1e6, -1e6, 1e9, -1e9, 1e30, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("T,E,topk,odd", [(40, 64, 8, False), (33, 5, 2, True), (20, 300, 4, False)])
+def test_probabilities_of_rows_far_from_zero(T, E, topk, odd, far):
+    """Adding a constant to a row changes no p: rows of equal logits and of a few steps of fp32
+    around a constant, whose log-sum-exp cannot hold log E beside it.  An exponential's
+    argument a is rounded to a 2^-24, its evaluation and the sum over E experts add at most
+    (E + 16) 2^-24, and the bracket's terms as much again."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.full((T, E), far)
+    step = max(abs(far) * 2.0 ** -22, 0.5)  # whole steps of fp32 there; each is exact
+    if abs(far) < 1e7:  # (past that a step is more than all of the softmax's range)
+        l[::2] += torch.randint(-3, 4, (l[::2].shape), generator=g) * step
+    b = Balance(T, E, topk, odd=odd, balance=1.0, z=0.0, logits=l).call()
+    d = b.get()[3].double().numpy()
+    want, size = gradient(l.double().numpy(), topk, 1.0, 0.0, float(np.float32(1.7)))
+    spread = (l.double().max(1, keepdim=True).values - l.double()).numpy()
+    tol = size * (2 * spread.max(1, keepdims=True) + 2 * E + 40) * e24 + 2.0 ** -125
+    assert (np.abs(d - want) <= tol).all(), np.max(np.abs(d - want) / tol)
+    # each row's gradient adds up to 0 (all of the experts' pulls cancel)
+    assert (np.abs(d.sum(1)) <= E * e24 * size.sum(1) + tol.sum(1)).all()
