@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(V > 4 ? 256 : 1024) balance_kernel(BalancePara
     int64_t t = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
     while (t < p.T) {
         // 32 tokens in fp32, then on to fp64 (whose conversions take four times as long)
-        float part[V], zpart = 0.0f;
+        float part[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) part[i] = 0.0f;
         for (int k = 0; k < 32 && t < p.T; ++k, t += step) {
@@ -229,14 +229,14 @@ __global__ void __launch_bounds__(V > 4 ? 256 : 1024) balance_kernel(BalancePara
             if (live) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) part[i] = __builtin_fmaf(e[i], inv, part[i]);
-                zpart = __builtin_fmaf(lse, lse, zpart);
+                // (in fp64 at once: a square may lie past fp32's range)
+                zsum = __builtin_fma((double)lse, (double)lse, zsum);
                 ++live_count;
             }
             if (in_group == 0) p.lse[t] = lse;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) psum[i] += (double)part[i];
-        zsum += (double)zpart;
     }
     // the groups of the wave
 #pragma unroll

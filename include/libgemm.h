@@ -555,8 +555,8 @@ int gemm_validate_moe(int64_t T, const gemm_moe_t *layer, const void *X, int64_t
  * gemm_moe_balance enqueues two kernels, gemm_moe_balance_grad one.  Both allocate
  * nothing, can be captured into a HIP graph, and give the same bits for the same call.
  *
- * Accuracy: softmax and logarithm are fp32 (a p below 2^-126 may be 0); sums over tokens
- * are fp32 over up to 32 of them and fp64 beyond; D is rounded once.
+ * Accuracy: softmax and logarithm are fp32 (a p below 2^-126 may be 0); sums of p over tokens are
+ * fp32 over up to 32 of them and fp64 beyond, those of lse^2 fp64; D is rounded once.
  *
  * Errors: GEMM_ERR_INVALID_DIM (T < 0 or above 2^31-1, E or topk < 1, topk > E),
  * GEMM_ERR_UNSUPPORTED (E > 1024, topk > 32, out_dtype; a weight that is not finite),

@@ -298,3 +298,27 @@ def test_probabilities_of_rows_far_from_zero(T, E, topk, odd, far):
     assert (np.abs(d - want) <= tol).all(), np.max(np.abs(d - want) / tol)
     # each row's gradient adds up to 0 (all of the experts' pulls cancel)
     assert (np.abs(d.sum(1)) <= E * e24 * size.sum(1) + tol.sum(1)).all()
+
+
+@pytest.mark.parametrize("z", [0.0, 1e-40, 0.5])
+def test_loss_of_rows_at_the_lowest_value(z):
+    """lse^2 of a row held at the type's lowest value does not fit fp32: loss[2] is Inf there,
+    and the weight decides whether loss[0] is."""
+    g = torch.Generator().manual_seed(3)
+    l = torch.randn(60, 10, generator=g)
+    l[4] = l[59] = torch.finfo(torch.float32).min
+    b = Balance(60, 10, 4, balance=0.5, z=z, logits=l).call()
+    loss = b.get()[0].double().numpy()
+    want = reference(l.double().numpy(), 4, np.ones(60), 0.5, float(np.float32(z)), 1.7)[0]
+    assert want[2] > 3.5e38 and loss[2] == np.inf
+    assert abs(loss[1] - want[1]) <= 1e-5 * want[1]
+    assert loss[0] == np.inf if want[0] > 3.5e38 else abs(loss[0] - want[0]) <= 1e-5 * want[0]
+
+
+def test_loss_of_large_squares():
+    """Squares that fit fp64 alone, and a mean that fits fp32."""
+    l = torch.zeros(4000, 4)
+    l[0] = -3e19  # 9e38 / 4000
+    loss = Balance(4000, 4, 2, balance=0.0, z=1.0, logits=l).call().get()[0].double().numpy()
+    want = 9e38 / 4000  # (the others' log(4)^2 is nothing beside it)
+    assert abs(loss[2] - want) <= 1e-6 * want and abs(loss[0] - want) <= 1e-6 * want
