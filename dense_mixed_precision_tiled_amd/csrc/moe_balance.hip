@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(BalanceParams p) {
         } else {
             // p = exp(l - lse) over its sum: lse is rounded, and where it is large beside log E its
             // rounding is a factor that all of a row's p share (E, for logits alike past 2^27 or so)
+            bool bad = false;
             float l[V], dot = 0.0f, sum = 0.0f;
             balance_load<V, VEC>(p.logits + t * p.ldl, e0, p.E, l);
 #pragma unroll
@@ -369,7 +370,20 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(BalanceParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) l[i] *= inv;
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[i] = g * l[i] * __builtin_fmaf(a, f[i] - dot, b * lse);
+            for (int i = 0; i < V; ++i) {
+                y[i] = g * l[i] * __builtin_fmaf(a, f[i] - dot, b * lse);
+                bad |= !__builtin_isfinite(y[i]);
+            }
+            // a factor may have left fp32's range (a weight times E, lse times a weight) where the
+            // result has not: once more in fp64
+            if (__ballot(bad)) {
+                const double gd = (double)(p.dloss ? *p.dloss : 1.0f) / (double)n;
+                const double ad = (double)p.balance * (double)p.E, bd = 2.0 * (double)p.z * (double)lse;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (!__builtin_isfinite(y[i]))
+                        y[i] = (float)(gd * (double)l[i] * __builtin_fma(ad, (double)(f[i] - dot), bd));
+            }
         }
 #pragma unroll
         for (int q = 0; q < V; q += 4) {

@@ -322,3 +322,26 @@ def test_loss_of_large_squares():
     loss = Balance(4000, 4, 2, balance=0.0, z=1.0, logits=l).call().get()[0].double().numpy()
     want = 9e38 / 4000  # (the others' log(4)^2 is nothing beside it)
     assert abs(loss[2] - want) <= 1e-6 * want and abs(loss[0] - want) <= 1e-6 * want
+
+
+@pytest.mark.parametrize("o", [F32, BF16])
+@pytest.mark.parametrize("balance,z", [(1.0, 1.0), (3e38, 0.0), (0.0, 3e38), (1e37, 1e37)])
+def test_gradients_whose_factors_leave_the_range(balance, z, o):
+    """Results that fit fp32, of products on the way that do not: a row at the type's lowest
+    value with a full z weight, and weights near fp32's largest on small p."""
+    g = torch.Generator().manual_seed(4)
+    T, E, topk = 6000, 64, 4
+    l = torch.randn(T, E, generator=g)
+    if z == 1.0:
+        l[5] = l[77] = torch.finfo(torch.float32).min
+    b = Balance(T, E, topk, o, balance=balance, z=z, logits=l, dloss=False).call()
+    d = b.get()[3].double().numpy()
+    want, size = gradient(l.double().numpy(), topk, float(np.float32(balance)), float(np.float32(z)), 1.0)
+    assert np.abs(want).max() < 3.3e38
+    spread = (l.double().max(1, keepdim=True).values - l.double()).numpy()
+    lse = np.abs(np.log(np.exp(l.double().numpy() - l.double().numpy().max(1, keepdims=True)).sum(1)) + l.double().numpy().max(1))
+    # (lse itself is off by (2 spread + E + 20) 2^-24, and by half a step of its own)
+    dlse = (2 * spread.max(1) + E + 20 + 4 * lse) * e24
+    tol = size * (2 * spread.max(1, keepdims=True) + 2 * E + 40) * e24 + (2 * z / T * dlse)[:, None] + 2.0 ** -125
+    tol = tol + HALF_STEP[o] * np.abs(want)
+    assert (np.abs(d - want) <= tol).all(), np.max(np.abs(d - want) / tol)
