@@ -345,3 +345,50 @@ def test_gradients_whose_factors_leave_the_range(balance, z, o):
     tol = size * (2 * spread.max(1, keepdims=True) + 2 * E + 40) * e24 + (2 * z / T * dlse)[:, None] + 2.0 ** -125
     tol = tol + HALF_STEP[o] * np.abs(want)
     assert (np.abs(d - want) <= tol).all(), np.max(np.abs(d - want) / tol)
+
+
+def test_many_tokens_for_each_thread():
+    """More than 32 tokens for each group of lanes, whose sums go on in fp64; compared with torch
+    in 64 bits on the device, to the bounds above (E = 3: p within 40 e, sums over tokens 34 e)."""
+    T, E, topk = 20000003, 3, 1
+    g = torch.Generator(device="cuda").manual_seed(0)
+    l = torch.randn(T, E, generator=g, device="cuda")
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.8).to(torch.uint8)
+    loss, counts, lse = torch.empty(3, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"), \
+        torch.empty(T, device="cuda")
+    D = torch.empty(T, E, device="cuda")
+    ws = torch.empty(lg.gemm_moe_balance_workspace(T, E, topk), dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_moe_balance(T, E, topk, l.data_ptr(), E, mask.data_ptr(), 1.0, 0.5, loss.data_ptr(), counts.data_ptr(),
+                           lse.data_ptr(), ws.data_ptr(), ws.numel(), stream()))
+    ok(lg.gemm_moe_balance_grad(T, E, topk, l.data_ptr(), E, mask.data_ptr(), 1.0, 0.5, counts.data_ptr(), lse.data_ptr(),
+                                0, D.data_ptr(), E, F32, stream()))
+    d = l.double()
+    live = mask != 0
+    n = int(live.sum())
+    c = torch.bincount(l[live].argmax(1), minlength=E)  # no ties among normal values of one row, or few
+    same = int(((l == l.max(1, keepdim=True).values).sum(1) > 1)[live].sum())
+    got = counts.long()
+    assert int(got[E]) == n and int((got[:E] - c).abs().sum()) <= 2 * same and int(got[:E].sum()) == n
+    p = torch.softmax(d, 1) * live[:, None]
+    f = got[:E].double() / n
+    want_lse = torch.logsumexp(d, 1) * live
+    b, z = float(E * (f * p.sum(0)).sum() / n), float((want_lse ** 2).sum() / n)
+    assert abs(float(loss[1]) - b) <= 80 * e24 * b and abs(float(loss[2]) - z) <= 200 * e24 * z
+    assert abs(float(loss[0]) - (b + 0.5 * z)) <= 200 * e24 * (b + 0.5 * z)
+    assert float((lse.double() - want_lse).abs().max()) <= 60 * e24 * 8
+    fp = (p * f).sum(1, keepdim=True)
+    assert bool((fp >= 0).all())
+    pull = E * (f - fp) + want_lse[:, None]
+    size = p * (E * (f + fp) + want_lse.abs()[:, None] + 1)
+    assert bool(((D.double() * n - p * pull).abs() <= 200 * e24 * size + 1e-30).all())
+
+
+@pytest.mark.parametrize("shift", [1, 100, 255])
+def test_workspace_at_any_address(shift):
+    b = Balance(3000, 40, 4)
+    clean = b.call().get()
+    ws = torch.full((b.size + 256,), 255, dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_moe_balance(b.T, b.E, b.topk, b.dl.ptr, b.dl.ld, 0, b.balance, b.z, b.loss.ptr, b.counts.ptr, b.lse.ptr,
+                           ws.data_ptr() + shift, b.size, stream()))
+    assert all(torch.equal(x, y) for x, y in zip(b.get(), clean))
+    assert (ws[:shift] == 255).all() and (ws[shift + b.size:] == 255).all()

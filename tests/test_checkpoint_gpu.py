@@ -572,3 +572,63 @@ def test_wgrad_overflowing_values_of_few_outputs(M, N, K, back, how):
     w, want = overflowing(M, N, K, [M - b for b in back], how)
     assert np.isinf(want[:, :32]).any() and np.isfinite(want[:, 32:]).all()
     assert np.array_equal(w.call().dD.get().double().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+@pytest.mark.parametrize("M,N,K", [(200, 16, 64), (200, 100, 192)])
+def test_wgrad_smallest_values(M, N, K, how):
+    """X^ far below bf16's smallest normal value: the products with a large G are exact."""
+    w = Wgrad(M, N, K, BF16, F32, how=how, ints=True)
+    w.S[:] = np.random.default_rng(0).integers(0, 3, size=w.S.shape)
+    w.dS.view.copy_(torch.from_numpy(w.S))
+    w.G = (w.G.float() * 2.0 ** 100).bfloat16()
+    w.dG.view.copy_(w.G)
+    want = w.G.double().numpy().T @ ck.values(w.Q, w.S)
+    assert np.array_equal(w.call().dD.get().double().numpy(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 16, 256), (1500, 200, 300)])
+@pytest.mark.parametrize("shift", [1, 100, 255])
+def test_wgrad_workspace_at_any_address(M, N, K, shift):
+    w = Wgrad(M, N, K)
+    assert w.size > 0
+    clean = w.call().dD.get()
+    ws = torch.full((w.size + 256,), 255, dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_checkpoint_wgrad(M, N, K, w.dG.ptr, w.dG.ld, w.dQ.ptr, w.dQ.ld, w.dS.ptr, w.dS.ld, 0, K, w.dD.ptr,
+                                w.dD.ld, w.i, w.o, ws.data_ptr() + shift, w.size, stream()))
+    assert torch.equal(w.dD.get(), clean)
+    assert (ws[:shift] == 255).all() and (ws[shift + w.size:] == 255).all()
+
+
+@pytest.mark.parametrize("N,K", [((1 << 27) + 130, 5), (3, (1 << 27) + 170)])
+def test_wgrad_more_than_one_launch(N, K):
+    """More rows or columns of D than one launch takes: integers, checked on the device."""
+    M = 3
+    g = torch.Generator(device="cuda").manual_seed(0)
+    G = torch.randint(-3, 4, (M, N), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    X = torch.randint(-3, 4, (M, K), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    Q, S = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, (K + 31) // 32, dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_checkpoint_pack(M, K, X.data_ptr(), K, BF16, Q.data_ptr(), K, S.data_ptr(), S.shape[1], stream()))
+    D = torch.full((N * K + 64,), 77.0, device="cuda")
+    size = lg.gemm_checkpoint_wgrad_workspace(M, N, K)
+    ws = torch.empty(size + 1, dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_checkpoint_wgrad(M, N, K, G.data_ptr(), N, Q.data_ptr(), K, S.data_ptr(), S.shape[1], 0, K, D.data_ptr(), K,
+                                BF16, F32, ws.data_ptr(), size, stream()))
+    assert (D[N * K:] == 77).all()
+    got = D[:N * K].view(N, K)
+    for n0 in range(0, N, 1 << 24):
+        for k0 in range(0, K, 1 << 24):
+            a, b = G[:, n0:n0 + (1 << 24)].float(), X[:, k0:k0 + (1 << 24)].float()
+            want = sum(a[m][:, None] * b[m][None, :] for m in range(M))
+            assert torch.equal(got[n0:n0 + (1 << 24), k0:k0 + (1 << 24)], want)
+
+
+def test_longest_row():
+    """A row of 2^31 - 1 values, packed and back."""
+    K = 2 ** 31 - 1
+    X = (torch.arange(K, dtype=torch.int32, device="cuda") % 61 - 30).bfloat16()
+    Q, S = torch.empty(K, dtype=torch.int8, device="cuda"), torch.empty((K + 31) // 32, dtype=torch.uint8, device="cuda")
+    D = torch.full((K + 9,), 77.0, dtype=torch.bfloat16, device="cuda")
+    ok(lg.gemm_checkpoint_pack(1, K, X.data_ptr(), K, BF16, Q.data_ptr(), K, S.data_ptr(), S.numel(), stream()))
+    ok(lg.gemm_checkpoint_unpack(1, K, Q.data_ptr(), K, S.data_ptr(), S.numel(), D.data_ptr(), K, BF16, stream()))
+    assert torch.equal(D[:K], X) and (D[K:] == 77).all()  # whole numbers below 64 are exact

@@ -429,3 +429,89 @@ def test_infinite_weights_give_infinities(T, i, o, how):
         assert np.array_equal(got[t, bad].double().numpy(), want.numpy(), equal_nan=True)
     w.call(w.dC)  # and in place
     assert np.array_equal(w.dC.get().double().numpy(), got.double().numpy(), equal_nan=True)
+
+
+@pytest.mark.parametrize("o", [F32, F16, BF16])
+@pytest.mark.parametrize("T", [20, 300])
+@pytest.mark.parametrize("size", ["large", "small", "mixed"])
+def test_fp16_inner_values_far_from_one(T, o, size):
+    """h at the ends of what fp16 operands reach (2^43 of a long row, 2^-42 of subnormal ones),
+    tokens of very different size in one tile, and tokens whose h is 0."""
+    K = 4096
+    w = Lora(T, K, 40, 16, 3, F16, o, c=False)
+    x = {"large": [60000.0], "small": [2.0 ** -20], "mixed": [60000.0, 2.0 ** -20, 1.0, 0.0]}[size]
+    w.X = (w.X.float().clamp(-1, 1) * torch.tensor(x).repeat(T)[:T, None]).half()
+    w.A = (w.A.float() * K ** 0.5).clamp(-1, 1) * {"large": 60000.0, "small": 2.0 ** -20, "mixed": 16.0}[size]
+    w.A = w.A.half()
+    if o != F32:  # results within the output's range
+        w.scales = w.scales * {"large": 2.0 ** -36, "small": 2.0 ** 36, "mixed": 2.0 ** -18}[size]
+        w.dscales.copy_(w.scales)
+    w.dX.view.copy_(w.X)
+    w.dA.view.copy_(w.A)
+    w.call().check()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_bf16_smallest_inner_values(T):
+    """Parts of h below bf16's smallest normal value still count."""
+    w = Lora(T, 64, 40, 16, 3, BF16, F32, c=False)
+    w.X, w.A = (w.X.float() * 2.0 ** -56).bfloat16(), (w.A.float() * 2.0 ** -56).bfloat16()
+    w.B = (w.B.float() * 2.0 ** 20).bfloat16()
+    w.scales = w.scales * 2.0 ** 90
+    for d, v in ((w.dX, w.X), (w.dA, w.A), (w.dB, w.B)):
+        d.view.copy_(v)
+    w.dscales.copy_(w.scales)
+    w.call().check()
+
+
+@pytest.mark.parametrize("how", ["vec", "odd"])
+def test_most_tokens(how):
+    """2^20 tokens, the most there can be: integers, checked on the device."""
+    T, K, N, rank, adapters = 1 << 20, 40, 24, 8, 7
+    pad = 3 if how == "odd" else 0
+    g = torch.Generator(device="cuda").manual_seed(0)
+    pick = lambda n, m: torch.randint(-2, 3, (n, m + pad), generator=g, device="cuda").bfloat16()  # noqa: E731
+    X, A, B, C = pick(T, K), pick(adapters * rank, K), pick(adapters * N, rank), pick(T, N)
+    ids = (torch.arange(T, device="cuda") // 999 % (adapters + 1) - 1).int()
+    D = torch.full((T + 1, N + pad), 77.0, device="cuda").bfloat16()
+    lora = lg.GemmLora(K, N, adapters, rank, A.data_ptr(), K + pad, B.data_ptr(), rank + pad)
+    ws = torch.empty(lg.gemm_lora_workspace(T, lora), dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_lora_run(T, lora, X.data_ptr(), K + pad, ids.data_ptr(), C.data_ptr(), N + pad, D.data_ptr(), N + pad,
+                        BF16, BF16, ws.data_ptr(), ws.numel(), stream()))
+    want = C[:, :N].float()
+    for a in range(adapters):
+        h = X[:, :K].float() @ A.float()[a * rank:(a + 1) * rank, :K].T
+        want += torch.where((ids == a)[:, None], h @ B.float()[a * N:(a + 1) * N, :rank].T, 0.0)
+    assert torch.equal(D[:T, :N], want.bfloat16()) and (D[T] == 77).all() and (D[:, N:] == 77).all()
+
+
+@pytest.mark.parametrize("T", [1, 20, 300])
+def test_widest(T):
+    """K and N of 2^19, the largest."""
+    K = N = 1 << 19
+    g = torch.Generator(device="cuda").manual_seed(T)
+    pick = lambda n, m, lo, hi: torch.randint(lo, hi, (n, m), generator=g, device="cuda").bfloat16()  # noqa: E731
+    X, A, B = pick(T, K, 0, 2), pick(2 * 5, K, -1, 2), torch.zeros(2 * N, 8, device="cuda").bfloat16()
+    B[:, :5] = pick(2 * N, 5, -1, 2)
+    ids = (torch.arange(T, device="cuda") // 40 % 2).int()
+    D = torch.full((T, N), 77.0, device="cuda")
+    lora = lg.GemmLora(K, N, 2, 5, A.data_ptr(), K, B.data_ptr(), 8)
+    ws = torch.empty(lg.gemm_lora_workspace(T, lora), dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_lora_run(T, lora, X.data_ptr(), K, ids.data_ptr(), 0, N, D.data_ptr(), N, BF16, F32, ws.data_ptr(),
+                        ws.numel(), stream()))
+    for a in (0, 1):
+        rows = torch.nonzero(ids == a).flatten()
+        h = X[rows].double() @ A[5 * a:5 * a + 5].double().T
+        assert torch.equal(D[rows].double(), h @ B[a * N:(a + 1) * N, :5].double().T)  # sums below 2^24: exact
+
+
+@pytest.mark.parametrize("T,N", [(16, 100), (80, 1100), (300, 136)])
+@pytest.mark.parametrize("shift", [1, 100, 255])
+def test_workspace_at_any_address(T, N, shift):
+    w = Lora(T, 1100, N, 12, 3, F16, F32)
+    clean = w.call().dD.get()
+    ws = torch.full((w.size + 256,), 255, dtype=torch.uint8, device="cuda")
+    ok(lg.gemm_lora_run(T, w.lora, w.dX.ptr, w.dX.ld, w.dids.data_ptr(), w.dC.ptr, w.dC.ld, w.dD.ptr, w.dD.ld, w.i,
+                        w.o, ws.data_ptr() + shift, w.size, stream()))
+    assert torch.equal(w.dD.get(), clean)
+    assert (ws[:shift] == 255).all() and (ws[shift + w.size:] == 255).all()
