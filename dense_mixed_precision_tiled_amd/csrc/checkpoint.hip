@@ -4,8 +4,10 @@
 // One pass over the data, bound by memory: a lane takes 8 values of a row (16 bytes
 // of a 16-bit type, 8 of Q), four lanes a block of 32.  The row of an item is found
 // with one multiplication, so that short and odd rows fill the waves too.  4096 x 16384
-// values of bf16 are packed in 41 us (5.0 TB/s, a copy's rate); D = G * gelu'(X^) of as many
-// takes 77 (4.4 TB/s; about 30 vector instructions for each value beside them).
+// values of bf16, call after call: packed in 41 us (5.0 TB/s, a copy's rate; fp32 61, 5.5 TB/s),
+// unpacked in 38 (5.3), D = G * gelu'(X^) in 68 to 74 (5.0 to 4.6; about 30 vector instructions for
+// each value beside the memory), with ReLU or SiLU 62 to 64.  Lines that are not whole 16 bytes
+// take three times as long (packing 113 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,8 +29,9 @@ struct CkParams {
     int K;
 };
 
-// Items of a thread, 256 apart.  (us of 4096 x 16384 values, packing and with GELU: two 41
-// and 74, four 46 and 83, eight 46 and 144, one 41 and 77; of 100 x 4104 3.2, four 4.3.)
+// Items of a thread, 256 apart.  (us of 4096 x 16384 values, packing, unpacking and with GELU: two
+// 42, 39 and 73, one 43, 49 and 74, four 47, 44 and 78, eight 49, 92 and 148; packing 100 x 4104 one
+// 3.4, two 4.3, four 6.3.)
 constexpr int kCkItems = 2;
 
 template <int DT>

@@ -12,9 +12,9 @@
 //
 // Three kernels: tiles for 16-byte aligned lines (wgrad.hpp), thin ones for up to 64 outputs
 // (wgrad_thin.hpp), and one for any alignment.  us: 16 x 4096 of 8192 tokens 13.2 and 2.4 for
-// the sums (memory; 2.7 TB/s); 1001 x 2056 of 3999 39 and 6 (420 TFLOP/s: 408 workgroups on
-// 512 places, edge tiles); 4096 x 4096 of 4096 with C 151 (910 TFLOP/s; bf16 operands of the
-// same layout 131, without Q to widen).
+// the sums (2.7 TB/s: latency); 1001 x 2056 of 3999 39 and 6 (420 TFLOP/s: 408 workgroups on
+// 512 places, edge tiles); 4096 x 4096 of 4096 with C 152 (900 TFLOP/s), without 142 (bf16
+// operands of the same layout 131, without Q to widen).  Any alignment: 117, 199 and 1196 without C.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

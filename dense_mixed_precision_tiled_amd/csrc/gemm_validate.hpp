@@ -296,11 +296,11 @@ inline int validate_lora_dims(int64_t T, const gemm_lora_t *l) {
     return GEMM_OK;
 }
 
-// Up to this many tokens they are taken one by one and 16 at a time, else 64 (lora.hpp).
+// Up to this many tokens they are taken one by one and 16 at a time, else 64 and 32 (lora.hpp).
 // us on 4096 x 4096 in bf16, first against second way: packed prompts of 4 adapters, 256
-// tokens, rank 16 17.4 and 19.5 (257), rank 64 40 and 23; 512 tokens 24 and 14.4, 59 and 17.3.
-// Tokens of 32 adapters in any order, as a decoding batch has them: 256 tokens 20 and 156, 53
-// and 191; 512 tokens 33 and 158, 90 and 199.
+// tokens, rank 16 18.5 and 20.9 (257), rank 64 42 and 24; 512 tokens 24 and 15.5, 59 and 18.4.
+// Tokens of 32 adapters in any order, as a decoding batch has them: 256 tokens 21 and 165, 55
+// and 212; 512 tokens 33 and 164, 90 and 211.
 constexpr int64_t kLoraFew = 256;
 // Parts of K that different workgroups take: with few tiles of tokens there are CUs to
 // spare, and an adapter's rows of A are long.
@@ -445,7 +445,7 @@ inline int validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int
 // are fitted to 290 measured (shape, tile, parts) of 24 shapes, 7% off in the mean, and the
 // plan takes 0.8% longer than the best measured one.  Measured (best of the other tile
 // beside it): 1001 x 2056 of 3999 128 in 3 40.4 (256 in 6 41.2; 128 whole 55); 512 x 512 of
-// 8192 128 in 16 19.9 (26.8); 4096 x 4096 of 4096 256 134.7 (184); 1024 x 4096 of 2048 128
+// 8192 128 in 16 19.9 (26.8); 4096 x 4096 of 4096 256 134.7, the least of its times (184); 1024 x 4096 of 2048 128
 // whole 36.8 (43.6; 128 in 2 41.1); 2048 x 2048 of 4096 128 in 2 59.1 (256 in 3 58.6).
 struct WgradPlan {
     int64_t bm, bn, splits, per;  // per: tokens of a part, a multiple of 64

@@ -15,14 +15,14 @@
 // Up to kLoraFew tokens (a decoding batch) what counts is latency: weights straight from
 // memory to the registers, for a few tokens in one kernel (lora_one_kernel), for more in two,
 // the first 16 tokens and an adapter for each workgroup, the second a token for each wave.
-// More tokens (prompts) are taken 64 at a time, and what counts is the data: X and A go
-// through LDS (read in the MFMA's own shape, a lane's 16 bytes are a request of their own, 64
-// cycles of a CU's address path for each KiB), and a wave of the second kernel keeps B's part
-// in registers for its 32 tokens.
+// More tokens (prompts) are taken 64 at a time by the first product and 32 by the second, and
+// what counts is the data: X and A go through LDS (read in the MFMA's own shape, a lane's 16
+// bytes are a request of their own, 64 cycles of a CU's address path for each KiB), and a wave of
+// the second kernel keeps B's part in registers for its 32 tokens.
 //
-// Kernels on 4096 x 4096 in bf16, us: one token, rank 16, 4.9; 64 tokens of 64 adapters 5.9
-// and 4.5 (16.8 MB of weights); 4096 tokens, rank 64, 8 adapters 16.2, 4.8 and 28 (2.1 and
-// 2.4 TB/s).
+// Kernels on 4096 x 4096 in bf16, us: one token, rank 16, 5.1; 64 tokens of 64 adapters 6.6
+// and 5.2 (16.8 MB of weights, from memory); 4096 tokens, rank 64, 8 adapters 17.2, 4.8 and 29.4
+// (2.0 and 2.3 TB/s).
 #pragma once
 
 #include "stream.hpp"
@@ -586,6 +586,7 @@ constexpr int kLoraUpTokens = 32;
 // first 29.3), z tiles.
 template <int IT, int OUT, int RS, bool VEC>
 __global__ void __launch_bounds__(256, OUT == DT_F32 ? 2 : RS == 2 || !VEC ? 3 : 4) lora_up_kernel(LoraParams p) {
+    static_assert(kLoraUpTokens <= 32, "a lane's values of a tile are the bits of `again`");
     constexpr int SUBS = kLoraUpTokens / 16, PARTS = kLoraParts<OUT>, OSZ = OUT == DT_F32 ? 4 : 2;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * 256 + wave * 64;

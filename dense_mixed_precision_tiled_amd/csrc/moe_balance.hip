@@ -14,9 +14,10 @@
 // brought to the sum 1.
 //
 // The first kernel is bound by its vector instructions (about 230 for four tokens of 64
-// experts, top 8, most of them the choice), the gradient by memory.  65536 tokens of 64
-// experts, top 8: 12.0 us (1.4 TB/s), 4.5 for the sums over the workgroups, and 8.8 for a
-// gradient in bf16 (2.9 TB/s); 1024 tokens of 8 experts 4.8, 2.7 and 3.1.
+// experts, top 8, most of them the choice), the gradient by latency: counts, lse and logits are
+// read one after the other.  65536 tokens of 64 experts, top 8, us: 12.0 to 13.4 (1.4 TB/s), 4.6
+// for the sums over the workgroups, and 8.9 to 9.7 for a gradient in bf16 (2.8 TB/s, half of a
+// copy's rate); 1024 tokens of 8 experts 4.9, 2.8 and 3.2.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

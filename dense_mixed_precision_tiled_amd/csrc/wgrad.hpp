@@ -16,8 +16,8 @@
 // What bounds it: the matrix units are busy 45% of the time at 4096^3.  In 64 tokens a wave
 // of the 256 x 256 tile issues 32 MFMAs and some 130 vector instructions, most of them
 // widening Q (sixteen times over, once for each tile row that reads it); the stages' barrier
-// leaves nothing else on the CU.  us, bf16 into fp32: 4096^3 135 without C (1.02 PFLOP/s; 131
-// for a product of bf16 operands of these layouts) and 151 with it; 128 x 128 tiles 184 there,
+// leaves nothing else on the CU.  us, bf16 into fp32: 4096^3 142 without C (970 TFLOP/s; 131
+// for a product of bf16 operands of these layouts) and 152 with it; 128 x 128 tiles 184 there,
 // but 37 against 59 for 1024 x 4096 of 2048 tokens, where they fill the CUs.
 #pragma once
 

@@ -12,8 +12,9 @@
 // their sums up in LDS.  G's rows and the blocks' units (fp32) of a stretch of tokens are
 // laid out in LDS before it: the loop reads them from there, G with the transposing reads.
 //
-// Bound by memory, and by its start: 16 x 4096 of 8192 tokens, 256 workgroups, takes 13.2 us,
-// 35 MB at 2.7 TB/s, with nothing to cover a workgroup's first loads of G, S and Q.
+// Bound by latency: 16 x 4096 of 8192 tokens, 256 workgroups, takes 13.2 us, 35 MB at 2.7 TB/s,
+// half of a copy's rate, with one workgroup on a CU and nothing to cover its first loads of G, S
+// and Q.
 #pragma once
 
 #include "wgrad.hpp"

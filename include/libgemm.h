@@ -555,6 +555,9 @@ int gemm_validate_moe(int64_t T, const gemm_moe_t *layer, const void *X, int64_t
  * gemm_moe_balance enqueues two kernels, gemm_moe_balance_grad one.  Both allocate
  * nothing, can be captured into a HIP graph, and give the same bits for the same call.
  *
+ * Logits of 16-byte aligned lines are read 16 bytes at a time: up to 12 bytes of the padding
+ * next to a row's last element too, also past the last row's.
+ *
  * Accuracy: softmax and logarithm are fp32 (a p below 2^-126 may be 0); sums of p over tokens are
  * fp32 over up to 32 of them and fp64 beyond, those of lse^2 fp64; D is rounded once.
  *
@@ -619,8 +622,9 @@ int gemm_validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const flo
  *                caller orders them.
  * The call enqueues one kernel (few tokens, rank 32 at most), two, or past 256 tokens three,
  * and allocates nothing, so it can be captured into a HIP graph; which tokens use which
- * adapter is found on the device, and a replay follows the ids of its own time.  Tokens do not touch each other: what an adapter
- * holds (an Inf, a NaN) reaches its own tokens only.  The same call gives the same bits.
+ * adapter is found on the device, and a replay follows the ids of its own time.  Tokens do
+ * not touch each other: what an adapter holds (an Inf, a NaN) reaches its own tokens only.
+ * The same call gives the same bits.
  *
  * Accuracy: products and sums are fp32, and D is rounded once.  Past 256 tokens the second
  * product takes h = x A^T as a sum of values of in_dtype: two of them for a 16-bit D (16
@@ -629,12 +633,14 @@ int gemm_validate_moe_balance_grad(int64_t T, int64_t E, int64_t topk, const flo
  * in fp32's range, and what is below 2^-38 of that largest value is lost.
  *
  * Speed: 16-byte loads of X and A where both are 16-byte aligned with lines of whole 16
- * bytes, of B alike, and (past 256 tokens) of C and D; element by element otherwise.  Up to
- * 256 tokens may use any adapters in any order (a decoding batch).  More of them are taken
- * in tiles of 64 consecutive ones, and an adapter's weights are read once for each tile that
- * it has tokens in: packed prompts.  There, adapters that change from token to token cost
- * that much more (512 tokens on 4096 x 4096, rank 16: 14 us in prompts of 4 adapters, 158
- * with 32 adapters mixed).
+ * bytes, of B alike, and (past 256 tokens) of C and D; element by element otherwise.  With
+ * them, up to 14 bytes of the padding next to a row's last element are read, also past the
+ * last row's, and never matter.  Up to 256 tokens may use any adapters in any order (a decoding
+ * batch).  More of them are taken in tiles of consecutive ones, 64 for A and 32 for B (16 past
+ * rank 64), and an adapter's A or B is read once for each tile that it has tokens in: packed
+ * prompts.  There, adapters that change from token to token cost that much more (512 tokens on
+ * 4096 x 4096, rank 16: 15 us in prompts of 4 adapters, 164 with 32 adapters mixed), and sums
+ * that are NaN, which are made again one by one, too.
  *
  * Errors: GEMM_ERR_INVALID_DIM (T < 0; K, N, adapters or rank < 1; K or N > 2^19),
  * GEMM_ERR_UNSUPPORTED (T > 2^20, adapters > 2^20, rank > 256, a dtype not named above),
@@ -715,8 +721,9 @@ int gemm_validate_lora(int64_t T, const gemm_lora_t *lora, const void *X, int64_
  *                (may be 0, then NULL is fine), of any content, owned by the caller,
  *                written by the call.  Calls that may overlap need workspaces of their own.
  * M, the tokens, is the reduction's length; with M == 0, D = C (or 0).  X^ is taken in
- * in_dtype (exact as said above; with GEMM_F16, values past 65504 become Inf), products
- * are exact and summed in fp32, and D is rounded once.  The same call gives the same bits.
+ * in_dtype (exact as said above; with GEMM_F16, values past 65504 become Inf, and those below
+ * 2^-14 are rounded to steps of 2^-24, which those of an fp16 X are), products are exact and
+ * summed in fp32, and D is rounded once.  The same call gives the same bits.
  *
  * Speed: 16-byte accesses where the operands' base pointers and lines are whole 16 bytes
  * (for wgrad G and Q, for the others X, G, D and Q); element by element otherwise.  With
