@@ -632,3 +632,17 @@ def test_longest_row():
     ok(lg.gemm_checkpoint_pack(1, K, X.data_ptr(), K, BF16, Q.data_ptr(), K, S.data_ptr(), S.numel(), stream()))
     ok(lg.gemm_checkpoint_unpack(1, K, Q.data_ptr(), K, S.data_ptr(), S.numel(), D.data_ptr(), K, BF16, stream()))
     assert torch.equal(D[:K], X) and (D[K:] == 77).all()  # whole numbers below 64 are exact
+
+
+@pytest.mark.parametrize("i,o,add", [(BF16, F32, True), (F16, F16, True), (BF16, BF16, False), (F16, F32, False)])
+def test_wgrad_whole_large_tiles(i, o, add):
+    """Tiles of 256 x 256 that take all of the tokens, a ragged number of them, and ragged edges."""
+    w = Wgrad(292, 2973, 2973, i, o, add=add)
+    assert w.size == 0
+    w.call().check()
+
+
+def test_wgrad_overflowing_values_in_whole_large_tiles():
+    w, want = overflowing(292, 2973, 2973, [252, 291], "vec")
+    assert np.isinf(want[:, :32]).any() and np.isfinite(want[:, 32:]).all()
+    assert np.array_equal(w.call().dD.get().double().numpy(), want, equal_nan=True)
