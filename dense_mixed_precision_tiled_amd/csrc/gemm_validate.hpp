@@ -445,8 +445,9 @@ inline int validate_checkpoint_act_grad(int64_t M, int64_t K, const void *Q, int
 // are fitted to 290 measured (shape, tile, parts) of 24 shapes, 7% off in the mean, and the
 // plan takes 0.8% longer than the best measured one.  Measured (best of the other tile
 // beside it): 1001 x 2056 of 3999 128 in 3 40.4 (256 in 6 41.2; 128 whole 55); 512 x 512 of
-// 8192 128 in 16 19.9 (26.8); 4096 x 4096 of 4096 256 134.7, the least of its times (184); 1024 x 4096 of 2048 128
-// whole 36.8 (43.6; 128 in 2 41.1); 2048 x 2048 of 4096 128 in 2 59.1 (256 in 3 58.6).
+// 8192 128 in 16 19.9 (26.8); 4096 x 4096 of 4096 256 134.7, the least of its times (184);
+// 1024 x 4096 of 2048 128 whole 36.8 (43.6; 128 in 2 41.1); 2048 x 2048 of 4096 128 in 2 59.1
+// (256 in 3 58.6).
 struct WgradPlan {
     int64_t bm, bn, splits, per;  // per: tokens of a part, a multiple of 64
 };

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) lora_down_kernel(LoraParams p) {
 
 // Many tokens: h of 64 tokens and 16 RT ranks.  64 values of k at a time through four LDS
 // stages, three of them on their way; a wave takes 16 of the tokens.  Bound by the loads in
-// flight: 4096 tokens, K = 4096, rank 64 take 16.2 us (X at 2.1 TB/s) in 256 workgroups, one
+// flight: 4096 tokens, K = 4096, rank 64 take 17.2 us (X at 2.0 TB/s) in 256 workgroups, one
 // on a CU, each waiting for its own stages.
 // Grid: x tiles, y chunks of 16 RT ranks, z parts of K.
 template <int IT, int RT>
@@ -567,8 +567,9 @@ __device__ __forceinline__ void lora_again(const LoraParams &p, int64_t t, int64
 
 // Tokens of a tile of the second product: with 64, the registers leave two waves a SIMD
 // instead of four (three past rank 32), whose loads, products and stores then follow one
-// another.  us, 64 and 32 tokens, N = 4096 in bf16: 512 tokens 9 and 6, 2048 of rank 32 11.6
-// and 10.2, 8192 of rank 16 37 and 33 (4.1 TB/s), 4096 of rank 64 28 and 28.
+// another.  us, 64 and 32 tokens, N = 4096 in bf16 (both without the search for NaN sums, which
+// adds 0.3 to 0.8): 512 tokens 9 and 6, 2048 of rank 32 11.6 and 10.2, 8192 of rank 16 37 and 33
+// (4.1 TB/s), 4096 of rank 64 28 and 28.
 constexpr int kLoraUpTokens = 32;
 
 // Many tokens: D of a tile and an adapter at a time; a wave takes 64 columns.  Its four

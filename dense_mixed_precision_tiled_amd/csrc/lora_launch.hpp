@@ -38,8 +38,9 @@ inline bool lora_one(const LoraParams &p) {
            (int64_t)p.K * (p.rank <= 16 ? 16 : 32) <= 1 << 18;
 }
 
-// few: 16 tokens at a time in the first product, one in the second.  vec_xa, vec_b: 16-byte loads of X and A, and of B.  Many
-// tokens without vec_xa take the first kernel of the few: its loads know any alignment.
+// few: 16 tokens at a time in the first product, one in the second.  vec_xa, vec_b: 16-byte
+// loads of X and A, and of B.  Many tokens without vec_xa take the first kernel of the few: its
+// loads know any alignment.
 template <int IT>
 hipError_t launch_lora(const LoraParams &p, int out_dtype, bool few, bool vec_xa, bool vec_b,
                        hipStream_t s) {
